@@ -1,7 +1,8 @@
 """MI355X (gfx950) MoE token dispatch / combine.
 
 A thin ctypes binding over ``libmoe_dispatch.so`` (HIP kernels behind the C
-ABI declared in ``include/moe_dispatch.h``).  The Python functions carry the
+ABI declared in ``include/moe_dispatch.h`` and, for the expert layer's
+operators, ``include/moe_experts.h``).  The Python functions carry the
 same names as the C entry points and only marshal arguments: torch tensors
 supply device memory and the current HIP stream, and every step of the path
 runs in the library's kernels.  There is no fallback: if the library is not
@@ -132,6 +133,17 @@ def _load():
     lib.moe_scale_words.restype = sz
     lib.moe_scales_mn_major.argtypes = [cfgp, i32, P, P, P]
     lib.moe_scales_mn_major.restype = ctypes.c_int
+    f32 = ctypes.c_float
+    lib.moe_rmsnorm.argtypes = [cfgp, i32, P, P, P, f32, P, P, P, P, P]
+    lib.moe_rmsnorm.restype = ctypes.c_int
+    lib.moe_expert_gemm.argtypes = [cfgp, i32, i32, i32, P, P, P, P, hp, P, P]
+    lib.moe_expert_gemm.restype = ctypes.c_int
+    lib.moe_expert_gemm_swiglu.argtypes = [cfgp, i32, i32, P, P, P, P, hp, P, P, P]
+    lib.moe_expert_gemm_swiglu.restype = ctypes.c_int
+    lib.moe_layer_workspace_bytes.argtypes = [cfgp, i32]
+    lib.moe_layer_workspace_bytes.restype = sz
+    lib.moe_layer_fused.argtypes = [cfgp, i32, i32, P, P, P, P, P, P, P, P, sz, P, P]
+    lib.moe_layer_fused.restype = ctypes.c_int
     lib.moe_status_str.argtypes = [ctypes.c_int]
     lib.moe_status_str.restype = ctypes.c_char_p
     _lib = lib
@@ -542,3 +554,123 @@ def moe_scales_mn_major(cfg: MoeConfig, rows: int, scale: torch.Tensor, scale_mn
     if scale_mn.numel() * scale_mn.element_size() < S * ld * 4:
         raise ValueError("scale_mn: fewer than S * ld words")
     _check("moe_scales_mn_major", lib.moe_scales_mn_major(ctypes.byref(cfg), int(rows), sp, op, _stream(stream)))
+
+
+# ---- expert-layer operators (include/moe_experts.h) ------------------------------
+
+LAYER_MAX_TOKENS = 64
+
+
+def _one_device(stream, **tensors) -> None:
+    """All tensors on the device the call launches on: the stream's, or the
+    current one's for a raw stream pointer."""
+    dev = getattr(stream, "device_index", None)
+    if dev is None:
+        dev = torch.cuda.current_device()
+    for name, t in tensors.items():
+        if t is not None and t.get_device() != dev:
+            raise ValueError(f"{name}: on device {t.device}, the call runs on device {dev}")
+    if dev != torch.cuda.current_device():
+        raise ValueError(f"the stream is on device {dev}, the current device is {torch.cuda.current_device()}")
+
+
+def _act_scale(quant: int, t: Optional[torch.Tensor], rows: int, n: int, name: str) -> Optional[int]:
+    """Scales of `rows` rows of `n` channels."""
+    nb = n // 128
+    elem, cols = {QUANT_FP8_F32: (4, nb), QUANT_FP8_UE8M0: (4, (nb + 3) // 4), QUANT_MXFP8: (1, n // 32)}[quant]
+    return _ptr(t, elem, rows * cols, name)
+
+
+def _weight_ptrs(cfg, w, w_scale, n: int, k: int, name: str):
+    """Weights [E, n, k] and their scales in cfg.quant's weight format."""
+    E, q = cfg.num_experts, cfg.quant
+    if q == QUANT_NONE:
+        if w_scale is not None:
+            raise ValueError(f"{name}_scale must be None for bf16 weights")
+        return _ptr(w, 2, E * n * k, name), None
+    rows = E * n if q == QUANT_MXFP8 else E * ((n + 127) // 128)
+    return _ptr(w, 1, E * n * k, name), _act_scale(q, w_scale, rows, k, name + "_scale")
+
+
+def moe_rmsnorm(cfg: MoeConfig, num_tokens: int, x: torch.Tensor, residual: Optional[torch.Tensor],
+                weight: torch.Tensor, eps: float, residual_out: Optional[torch.Tensor],
+                out: Optional[torch.Tensor], out_q: Optional[torch.Tensor] = None,
+                out_scale: Optional[torch.Tensor] = None, stream=None) -> None:
+    """r = bf16(x + residual); y = r / sqrt(mean(r^2) + eps) * weight, stored
+    as bf16 (out) and/or quantized as the dispatch quantizes (out_q, out_scale)."""
+    lib = _load()
+    n = num_tokens * cfg.hidden
+    _one_device(stream, x=x, residual=residual, weight=weight, residual_out=residual_out, out=out, out_q=out_q,
+                out_scale=out_scale)
+    if out_scale is not None and cfg.quant == QUANT_NONE:
+        raise ValueError("out_scale must be None without FP8 quantization")
+    _check("moe_rmsnorm", lib.moe_rmsnorm(
+        ctypes.byref(cfg), int(num_tokens), _ptr(x, 2, n, "x"), _ptr(residual, 2, n, "residual"),
+        _ptr(weight, 2, cfg.hidden, "weight"), float(eps), _ptr(residual_out, 2, n, "residual_out"),
+        _ptr(out, 2, n, "out"), _ptr(out_q, 1, n, "out_q"),
+        None if out_scale is None else _act_scale(cfg.quant, out_scale, num_tokens, cfg.hidden, "out_scale"),
+        _stream(stream)))
+
+
+def _gemm_rows(cfg, num_tokens, handle):
+    return int(num_tokens) if handle is None else moe_rows_capacity(cfg)
+
+
+def moe_expert_gemm(cfg: MoeConfig, num_tokens: int, n: int, k: int, a: torch.Tensor, a_scale: torch.Tensor,
+                    w: torch.Tensor, w_scale: torch.Tensor, handle: Optional[Handle], y: torch.Tensor,
+                    stream=None) -> None:
+    """y[row] = a[row] @ w[e].T for the dispatched rows of every expert e, FP8
+    with block scales, bf16 out; handle None: one dense product over num_tokens rows."""
+    lib = _load()
+    if cfg.quant == QUANT_NONE:
+        raise MoeError("moe_expert_gemm", MOE_ERR_UNSUPPORTED)
+    rows = _gemm_rows(cfg, num_tokens, handle)
+    _one_device(stream, a=a, a_scale=a_scale, w=w, w_scale=w_scale, y=y,
+                handle=None if handle is None else handle.recv_count)
+    wp, wsp = _weight_ptrs(cfg, w, w_scale, n, k, "w")
+    _check("moe_expert_gemm", lib.moe_expert_gemm(
+        ctypes.byref(cfg), int(num_tokens), int(n), int(k), _ptr(a, 1, rows * k, "a"),
+        _act_scale(cfg.quant, a_scale, rows, k, "a_scale"), wp, wsp,
+        None if handle is None else ctypes.byref(handle.c), _ptr(y, 2, rows * n, "y"), _stream(stream)))
+
+
+def moe_expert_gemm_swiglu(cfg: MoeConfig, num_tokens: int, inter: int, a: torch.Tensor, a_scale: torch.Tensor,
+                           w13: torch.Tensor, w13_scale: torch.Tensor, handle: Optional[Handle], h: torch.Tensor,
+                           h_scale: torch.Tensor, stream=None) -> None:
+    """(h, h_scale)[row] = quantize(silu(gate) * up) with gate and up the two
+    halves of a[row] @ w13[e].T."""
+    lib = _load()
+    if cfg.quant == QUANT_NONE:
+        raise MoeError("moe_expert_gemm_swiglu", MOE_ERR_UNSUPPORTED)
+    rows, H = _gemm_rows(cfg, num_tokens, handle), cfg.hidden
+    _one_device(stream, a=a, a_scale=a_scale, w13=w13, w13_scale=w13_scale, h=h, h_scale=h_scale,
+                handle=None if handle is None else handle.recv_count)
+    wp, wsp = _weight_ptrs(cfg, w13, w13_scale, 2 * inter, H, "w13")
+    _check("moe_expert_gemm_swiglu", lib.moe_expert_gemm_swiglu(
+        ctypes.byref(cfg), int(num_tokens), int(inter), _ptr(a, 1, rows * H, "a"),
+        _act_scale(cfg.quant, a_scale, rows, H, "a_scale"), wp, wsp,
+        None if handle is None else ctypes.byref(handle.c), _ptr(h, 1, rows * inter, "h"),
+        _act_scale(cfg.quant, h_scale, rows, inter, "h_scale"), _stream(stream)))
+
+
+def moe_layer_workspace_bytes(cfg: MoeConfig, inter: int) -> int:
+    return int(_load().moe_layer_workspace_bytes(ctypes.byref(cfg), int(inter)))
+
+
+def moe_layer_fused(cfg: MoeConfig, num_tokens: int, inter: int, topk_idx: torch.Tensor, topk_w: torch.Tensor,
+                    x: torch.Tensor, w13: torch.Tensor, w13_scale: Optional[torch.Tensor], w2: torch.Tensor,
+                    w2_scale: Optional[torch.Tensor], workspace: torch.Tensor, out: torch.Tensor,
+                    stream=None) -> None:
+    """out[t] = sum_k topk_w[t,k] * W2[e] (silu(W13g[e] x[t]) * (W13u[e] x[t]))
+    for at most LAYER_MAX_TOKENS tokens, in two kernels."""
+    lib = _load()
+    H, P = cfg.hidden, num_tokens * cfg.num_topk
+    _one_device(stream, topk_idx=topk_idx, topk_w=topk_w, x=x, w13=w13, w13_scale=w13_scale, w2=w2,
+                w2_scale=w2_scale, workspace=workspace, out=out)
+    w13p, w13s = _weight_ptrs(cfg, w13, w13_scale, 2 * inter, H, "w13")
+    w2p, w2s = _weight_ptrs(cfg, w2, w2_scale, H, inter, "w2")
+    _check("moe_layer_fused", lib.moe_layer_fused(
+        ctypes.byref(cfg), int(num_tokens), int(inter), _ptr(topk_idx, 4, P, "topk_idx"),
+        _ptr(topk_w, 4, P, "topk_w"), _ptr(x, 2, num_tokens * H, "x"), w13p, w13s, w2p, w2s,
+        _ptr(workspace, None, 0, "workspace"), workspace.numel() * workspace.element_size(),
+        _ptr(out, 2, num_tokens * H, "out"), _stream(stream)))

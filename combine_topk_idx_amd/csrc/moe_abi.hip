@@ -10,7 +10,7 @@
 #include <atomic>
 #include <mutex>
 
-#include "moe_internal.h"
+#include "moe_experts_internal.h"
 
 namespace moe {
 
@@ -55,9 +55,11 @@ void *scratch_address(int dev)
     return q;
 }
 
+}  // namespace
+
 bool aligned(const void *p, size_t a) { return ((uintptr_t)p % a) == 0; }
 
-int64_t rows_capacity64(const moe_config_t &c)
+static int64_t rows_capacity64(const moe_config_t &c)
 {
     if (c.layout == MOE_LAYOUT_CONTIGUOUS)
         return (int64_t)c.max_tokens * c.num_topk + (int64_t)c.num_experts * (c.align - 1);
@@ -106,6 +108,17 @@ moe_status_t check_handle(const moe_handle_t *h)
             return MOE_ERR_INVALID_ARG;
     return MOE_OK;
 }
+
+moe_status_t check_tokens(const moe_config_t &c, int32_t num_tokens)
+{
+    if (num_tokens < 0)
+        return MOE_ERR_INVALID_ARG;
+    if (num_tokens > c.max_tokens)
+        return MOE_ERR_CAPACITY;
+    return MOE_OK;
+}
+
+namespace {
 
 moe_status_t check_rank_handle(const moe_rank_handle_t *h)
 {
@@ -158,15 +171,6 @@ moe_status_t check_dedup(const moe_config_t *cfg, int32_t num_tokens, const moe_
     if (num_tokens < 0)
         return MOE_ERR_INVALID_ARG;
     if (num_tokens > cfg->max_tokens)
-        return MOE_ERR_CAPACITY;
-    return MOE_OK;
-}
-
-moe_status_t check_tokens(const moe_config_t &c, int32_t num_tokens)
-{
-    if (num_tokens < 0)
-        return MOE_ERR_INVALID_ARG;
-    if (num_tokens > c.max_tokens)
         return MOE_ERR_CAPACITY;
     return MOE_OK;
 }

@@ -1,0 +1,70 @@
+// Device building blocks of the expert products: matrix-instruction fragments,
+// block scales, and the E4M3 quantization of a row group held in registers.
+#pragma once
+
+#include "moe_device.h"
+#include "moe_experts_internal.h"
+
+namespace moe {
+namespace dev {
+
+typedef int i32x8 __attribute__((ext_vector_type(8)));
+typedef int i32x4 __attribute__((ext_vector_type(4)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+
+constexpr bool per_row_weight_scale(int quant) { return quant == MOE_QUANT_MXFP8; }
+
+// One operand of v_mfma_f32_16x16x128_f8f6f4: lane l holds row (l & 15), and of
+// that row's 128 channels the 16 bytes at 16 * (l >> 4) and at 64 + 16 * (l >> 4)
+// -- the order in which the instruction counts channels, and in memory two
+// loads that cover 64 contiguous bytes of each of 16 rows.
+__device__ __forceinline__ i32x8 load_frag(const uint8_t *row_k, int g)
+{
+    const u32x4 lo = *reinterpret_cast<const u32x4 *>(row_k + 16 * g);
+    const u32x4 hi = *reinterpret_cast<const u32x4 *>(row_k + 64 + 16 * g);
+    return i32x8{(int)lo[0], (int)lo[1], (int)lo[2], (int)lo[3], (int)hi[0], (int)hi[1], (int)hi[2], (int)hi[3]};
+}
+
+// fp32 -> bf16 bits, round to nearest even (finite values and infinities).
+__device__ __forceinline__ uint32_t bf16_bits(float f)
+{
+    return __builtin_bit_cast(uint16_t, (__bf16)f);
+}
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) { return bf16_bits(lo) | bf16_bits(hi) << 16; }
+
+// silu(g) * u
+__device__ __forceinline__ float swiglu(float g, float u) { return g / (1.0f + expf(-g)) * u; }
+
+// The scale of a block with largest magnitude `amax`, the factor that E4M3
+// values are made with, and how the scale is stored -- the rules of the
+// dispatch (store_item in moe_device.h).
+template <int QUANT>
+struct BlockScale {
+    float s;        // FP8_F32: values are divided by it; power-of-two formats: multiplied by it
+    uint32_t byte;  // power-of-two formats: the stored exponent byte
+    __device__ __forceinline__ explicit BlockScale(float amax)
+    {
+        const float af = fmaxf(amax, 1e-10f);
+        byte = 0;
+        if constexpr (QUANT == MOE_QUANT_FP8_F32) {
+            s = af / 448.0f;
+        } else {
+            const uint32_t ab = __float_as_uint(af);
+            int e = (int)(ab >> 23) - 127 - 8;
+            if (QUANT == MOE_QUANT_FP8_UE8M0)
+                e += (ab & 0x7FFFFFu) > 0x600000u ? 1 : 0;
+            s = __uint_as_float((uint32_t)(127 - e) << 23);
+            byte = (uint32_t)(e + 127);
+        }
+    }
+    __device__ __forceinline__ float apply(float v) const
+    {
+        const float d = QUANT == MOE_QUANT_FP8_F32 ? v / s : v * s;
+        return fminf(fmaxf(d, -448.0f), 448.0f);
+    }
+};
+
+}  // namespace dev
+}  // namespace moe

@@ -1,0 +1,183 @@
+// Residual add + root-mean-square norm on gfx950, with the normed rows in 8
+// bits beside or instead of bf16.
+//
+//   r = bf16(x + residual), y = r / sqrt(mean(r^2) + eps) * weight
+//
+// One pass: a row stays in its threads' registers between the sum of squares
+// and the outputs, so every input is read once and every output written once.
+// Lanes hold 8 channels (one 16-byte load), so a 128-channel quantization block
+// is 16 adjacent lanes -- one DPP row -- and an MX block of 32 is one quad.
+#include "moe_mma.h"
+
+namespace moe {
+
+namespace {
+
+// max over a row of 16 lanes
+__device__ __forceinline__ float max16(float v)
+{
+    v = dev::max8(v);
+    return fmaxf(v, dev::dpp<0x140>(v));  // row_mirror: the other half of the row
+}
+
+__device__ __forceinline__ float wave_sum(float v)
+{
+#pragma unroll
+    for (int m = 1; m < kWave; m <<= 1)
+        v += __shfl_xor(v, m);
+    return v;
+}
+
+// A row is handled by THREADS threads with up to NV vectors of 8 channels each
+// (H <= 8 * THREADS * NV); the block holds ROWS rows.
+template <int QUANT, int THREADS, int ROWS, int NV>
+__global__ __launch_bounds__(THREADS *ROWS) void rmsnorm_kernel(NormArgs a)
+{
+    constexpr int kWaves = THREADS / kWave;
+    __shared__ float red[ROWS][kWaves];
+    const int sub = ROWS == 1 ? 0 : threadIdx.x / THREADS;
+    const int tid = threadIdx.x - sub * THREADS;
+    const int lane = tid & (kWave - 1);
+    const int64_t t = (int64_t)blockIdx.x * ROWS + sub;
+    const bool live = ROWS == 1 || t < a.T;
+    const int nvec = a.H / 8;
+    const int64_t base = t * a.H;
+
+    uint4 v[NV], wv[NV], rv[NV];
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        const int c = (i * THREADS + tid) * 8;
+        if (live && c < a.H) {
+            v[i] = *reinterpret_cast<const uint4 *>(a.x + base + c);
+            if (a.residual != nullptr)
+                rv[i] = *reinterpret_cast<const uint4 *>(a.residual + base + c);
+            wv[i] = *reinterpret_cast<const uint4 *>(a.weight + c);
+        } else {
+            v[i] = rv[i] = wv[i] = make_uint4(0, 0, 0, 0);
+        }
+    }
+    float sum = 0.0f;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        uint32_t *p = reinterpret_cast<uint32_t *>(&v[i]);
+        const uint32_t *q = reinterpret_cast<const uint32_t *>(&rv[i]);
+        if (a.residual != nullptr) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                p[j] = dev::pack_bf16(dev::bf16_lo(p[j]) + dev::bf16_lo(q[j]),
+                                      dev::bf16_hi(p[j]) + dev::bf16_hi(q[j]));
+            const int c = (i * THREADS + tid) * 8;
+            if (live && c < a.H)
+                *reinterpret_cast<uint4 *>(a.residual_out + base + c) = v[i];
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const float lo = dev::bf16_lo(p[j]), hi = dev::bf16_hi(p[j]);
+            sum = __builtin_fmaf(lo, lo, sum);
+            sum = __builtin_fmaf(hi, hi, sum);
+        }
+    }
+    sum = wave_sum(sum);
+    if constexpr (kWaves > 1) {
+        if (lane == 0)
+            red[sub][tid / kWave] = sum;
+        __syncthreads();
+        sum = 0.0f;
+#pragma unroll
+        for (int w = 0; w < kWaves; ++w)
+            sum += red[sub][w];
+    }
+    const float inv = 1.0f / sqrtf(sum / (float)a.H + a.eps);
+
+    const int NB = a.H / kQuantGroup;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        const int vec = i * THREADS + tid;
+        const int c = vec * 8;
+        const bool on = live && vec < nvec;
+        const uint32_t *p = reinterpret_cast<const uint32_t *>(&v[i]);
+        const uint32_t *w = reinterpret_cast<const uint32_t *>(&wv[i]);
+        float y[8];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            y[2 * j] = dev::bf16_lo(p[j]) * inv * dev::bf16_lo(w[j]);
+            y[2 * j + 1] = dev::bf16_hi(p[j]) * inv * dev::bf16_hi(w[j]);
+        }
+        if (on && a.out != nullptr)
+            *reinterpret_cast<uint4 *>(a.out + base + c) =
+                make_uint4(dev::pack_bf16(y[0], y[1]), dev::pack_bf16(y[2], y[3]), dev::pack_bf16(y[4], y[5]),
+                           dev::pack_bf16(y[6], y[7]));
+        if constexpr (QUANT != MOE_QUANT_NONE) {
+            float amax = 0.0f;
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                amax = fmaxf(amax, fabsf(y[j]));
+            if constexpr (QUANT == MOE_QUANT_MXFP8) {
+                amax = fmaxf(amax, dev::dpp<0xB1>(amax));
+                amax = fmaxf(amax, dev::dpp<0x4E>(amax));
+            } else {
+                amax = max16(amax);
+            }
+            const dev::BlockScale<QUANT> bs(amax);
+            float d[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                d[j] = bs.apply(y[j]);
+            if (on) {
+                *reinterpret_cast<uint2 *>(a.out_q + base + c) =
+                    make_uint2(dev::pack_e4m3(d[0], d[1], d[2], d[3]), dev::pack_e4m3(d[4], d[5], d[6], d[7]));
+                if constexpr (QUANT == MOE_QUANT_FP8_F32) {
+                    if ((vec & 15) == 0)
+                        static_cast<float *>(a.out_scale)[t * NB + (vec >> 4)] = bs.s;
+                } else if constexpr (QUANT == MOE_QUANT_MXFP8) {
+                    if ((vec & 3) == 0)
+                        static_cast<uint8_t *>(a.out_scale)[t * (a.H / 32) + (vec >> 2)] = (uint8_t)bs.byte;
+                } else {
+                    const int blk = vec >> 4;
+                    uint8_t *row = static_cast<uint8_t *>(a.out_scale) + t * ((NB + 3) / 4 * 4);
+                    if ((vec & 15) == 0)
+                        row[blk] = (uint8_t)bs.byte;
+                    // the last word's unused high bytes are 0
+                    if (blk == NB - 1 && (vec & 15) > 0 && blk + (vec & 15) < (NB + 3) / 4 * 4)
+                        row[blk + (vec & 15)] = 0;
+                }
+            }
+        }
+    }
+}
+
+template <int QUANT, int THREADS, int ROWS, int NV>
+hipError_t launch(const NormArgs &a, hipStream_t stream)
+{
+    const dim3 grid((a.T + ROWS - 1) / ROWS), block(THREADS * ROWS);
+    hipLaunchKernelGGL((rmsnorm_kernel<QUANT, THREADS, ROWS, NV>), grid, block, 0, stream, a);
+    return hipGetLastError();
+}
+
+template <int QUANT>
+hipError_t launch_quant(const NormArgs &a, hipStream_t stream)
+{
+    if (a.H <= 2048)
+        return launch<QUANT, 64, 4, 4>(a, stream);
+    if (a.H <= 8192)
+        return launch<QUANT, 256, 1, 4>(a, stream);
+    return launch<QUANT, 1024, 1, 4>(a, stream);
+}
+
+}  // namespace
+
+hipError_t launch_rmsnorm(const NormArgs &a, int32_t quant, hipStream_t stream)
+{
+    if (a.out_q == nullptr)
+        return launch_quant<MOE_QUANT_NONE>(a, stream);
+    switch (quant) {
+    case MOE_QUANT_FP8_F32:
+        return launch_quant<MOE_QUANT_FP8_F32>(a, stream);
+    case MOE_QUANT_FP8_UE8M0:
+        return launch_quant<MOE_QUANT_FP8_UE8M0>(a, stream);
+    default:
+        return launch_quant<MOE_QUANT_MXFP8>(a, stream);
+    }
+}
+
+}  // namespace moe
