@@ -29,6 +29,8 @@ hipError_t launch_rmsnorm(const NormArgs &a, int32_t quant, hipStream_t stream);
 
 // ---- grouped products -----------------------------------------------------------
 
+constexpr int32_t kMaxGemmK = 1 << 22;  // input channels of a product: 256 rows stay below 2 GiB
+
 struct ExpertGemmArgs {
     const uint8_t *a;              // [rows, k] E4M3
     const void *a_scale;
