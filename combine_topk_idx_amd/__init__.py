@@ -561,35 +561,51 @@ def moe_scales_mn_major(cfg: MoeConfig, rows: int, scale: torch.Tensor, scale_mn
 LAYER_MAX_TOKENS = 64
 
 
-def _one_device(stream, **tensors) -> None:
-    """All tensors on the device the call launches on: the stream's, or the
-    current one's for a raw stream pointer."""
-    dev = getattr(stream, "device_index", None)
-    if dev is None:
-        dev = torch.cuda.current_device()
-    for name, t in tensors.items():
-        if t is not None and t.get_device() != dev:
-            raise ValueError(f"{name}: on device {t.device}, the call runs on device {dev}")
-    if dev != torch.cuda.current_device():
-        raise ValueError(f"the stream is on device {dev}, the current device is {torch.cuda.current_device()}")
+def _device(stream) -> int:
+    """The device a call runs on: the current one, which must be the stream's."""
+    dev = torch._C._cuda_getDevice()
+    at = getattr(stream, "device_index", dev)
+    if at != dev:
+        raise ValueError(f"the stream is on device {at}, the current device is {dev}")
+    return dev
 
 
-def _act_scale(quant: int, t: Optional[torch.Tensor], rows: int, n: int, name: str) -> Optional[int]:
-    """Scales of `rows` rows of `n` channels."""
-    nb = n // 128
-    elem, cols = {QUANT_FP8_F32: (4, nb), QUANT_FP8_UE8M0: (4, (nb + 3) // 4), QUANT_MXFP8: (1, n // 32)}[quant]
-    return _ptr(t, elem, rows * cols, name)
+def _raw_stream(stream, dev: int) -> int:
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(dev)
+    return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
-def _weight_ptrs(cfg, w, w_scale, n: int, k: int, name: str):
-    """Weights [E, n, k] and their scales in cfg.quant's weight format."""
-    E, q = cfg.num_experts, cfg.quant
-    if q == QUANT_NONE:
-        if w_scale is not None:
-            raise ValueError(f"{name}_scale must be None for bf16 weights")
-        return _ptr(w, 2, E * n * k, name), None
-    rows = E * n if q == QUANT_MXFP8 else E * ((n + 127) // 128)
-    return _ptr(w, 1, E * n * k, name), _act_scale(q, w_scale, rows, k, name + "_scale")
+def _arg(t: Optional[torch.Tensor], dev: int, elem: int, n: int, name: str) -> Optional[int]:
+    """Address of a dense tensor of at least n elements of `elem` bytes on device dev."""
+    if t is None:
+        return None
+    if t.get_device() == dev and t.is_contiguous() and t.element_size() == elem and t.numel() >= n:
+        return t.data_ptr()
+    if t.get_device() != dev:
+        raise ValueError(f"{name}: on device {t.device}, the call runs on device {dev}")
+    return _ptr(t, elem, n, name)  # says what is wrong
+
+
+# Per row of n channels: element size of the scales and how many there are.
+_ROW_SCALES = {QUANT_FP8_F32: lambda n: (4, n // 128), QUANT_FP8_UE8M0: lambda n: (4, (n // 128 + 3) // 4),
+               QUANT_MXFP8: lambda n: (1, n // 32)}
+
+
+def _row_scales(quant: int, t: Optional[torch.Tensor], dev: int, rows: int, n: int, name: str) -> Optional[int]:
+    """Scales of `rows` rows of `n` channels (None without FP8)."""
+    if quant == QUANT_NONE:
+        if t is not None:
+            raise ValueError(f"{name} must be None without FP8 quantization")
+        return None
+    elem, cols = _ROW_SCALES[quant](n)
+    return _arg(t, dev, elem, rows * cols, name)
+
+
+def _weight_scales(cfg, t, dev: int, n: int, k: int, name: str) -> Optional[int]:
+    """Scales of weights [E, n, k]: a row per channel (MXFP8) or per 128 channels."""
+    rows = n if cfg.quant == QUANT_MXFP8 else (n + 127) // 128
+    return _row_scales(cfg.quant, t, dev, cfg.num_experts * rows, k, name)
 
 
 def moe_rmsnorm(cfg: MoeConfig, num_tokens: int, x: torch.Tensor, residual: Optional[torch.Tensor],
@@ -598,22 +614,15 @@ def moe_rmsnorm(cfg: MoeConfig, num_tokens: int, x: torch.Tensor, residual: Opti
                 out_scale: Optional[torch.Tensor] = None, stream=None) -> None:
     """r = bf16(x + residual); y = r / sqrt(mean(r^2) + eps) * weight, stored
     as bf16 (out) and/or quantized as the dispatch quantizes (out_q, out_scale)."""
-    lib = _load()
-    n = num_tokens * cfg.hidden
-    _one_device(stream, x=x, residual=residual, weight=weight, residual_out=residual_out, out=out, out_q=out_q,
-                out_scale=out_scale)
-    if out_scale is not None and cfg.quant == QUANT_NONE:
-        raise ValueError("out_scale must be None without FP8 quantization")
-    _check("moe_rmsnorm", lib.moe_rmsnorm(
-        ctypes.byref(cfg), int(num_tokens), _ptr(x, 2, n, "x"), _ptr(residual, 2, n, "residual"),
-        _ptr(weight, 2, cfg.hidden, "weight"), float(eps), _ptr(residual_out, 2, n, "residual_out"),
-        _ptr(out, 2, n, "out"), _ptr(out_q, 1, n, "out_q"),
-        None if out_scale is None else _act_scale(cfg.quant, out_scale, num_tokens, cfg.hidden, "out_scale"),
-        _stream(stream)))
-
-
-def _gemm_rows(cfg, num_tokens, handle):
-    return int(num_tokens) if handle is None else moe_rows_capacity(cfg)
+    dev, H = _device(stream), cfg.hidden
+    n = num_tokens * H
+    code = _load().moe_rmsnorm(
+        ctypes.byref(cfg), num_tokens, _arg(x, dev, 2, n, "x"), _arg(residual, dev, 2, n, "residual"),
+        _arg(weight, dev, 2, H, "weight"), eps, _arg(residual_out, dev, 2, n, "residual_out"),
+        _arg(out, dev, 2, n, "out"), _arg(out_q, dev, 1, n, "out_q"),
+        _row_scales(cfg.quant, out_scale, dev, num_tokens, H, "out_scale"), _raw_stream(stream, dev))
+    if code:
+        raise MoeError("moe_rmsnorm", code)
 
 
 def moe_expert_gemm(cfg: MoeConfig, num_tokens: int, n: int, k: int, a: torch.Tensor, a_scale: torch.Tensor,
@@ -621,17 +630,22 @@ def moe_expert_gemm(cfg: MoeConfig, num_tokens: int, n: int, k: int, a: torch.Te
                     stream=None) -> None:
     """y[row] = a[row] @ w[e].T for the dispatched rows of every expert e, FP8
     with block scales, bf16 out; handle None: one dense product over num_tokens rows."""
-    lib = _load()
     if cfg.quant == QUANT_NONE:
         raise MoeError("moe_expert_gemm", MOE_ERR_UNSUPPORTED)
-    rows = _gemm_rows(cfg, num_tokens, handle)
-    _one_device(stream, a=a, a_scale=a_scale, w=w, w_scale=w_scale, y=y,
-                handle=None if handle is None else handle.recv_count)
-    wp, wsp = _weight_ptrs(cfg, w, w_scale, n, k, "w")
-    _check("moe_expert_gemm", lib.moe_expert_gemm(
-        ctypes.byref(cfg), int(num_tokens), int(n), int(k), _ptr(a, 1, rows * k, "a"),
-        _act_scale(cfg.quant, a_scale, rows, k, "a_scale"), wp, wsp,
-        None if handle is None else ctypes.byref(handle.c), _ptr(y, 2, rows * n, "y"), _stream(stream)))
+    dev, q = _device(stream), cfg.quant
+    hp = None
+    rows = num_tokens
+    if handle is not None:
+        rows = moe_rows_capacity(cfg)
+        _arg(handle.recv_count, dev, 4, cfg.num_experts, "handle")
+        hp = ctypes.byref(handle.c)
+    code = _load().moe_expert_gemm(
+        ctypes.byref(cfg), num_tokens, n, k, _arg(a, dev, 1, rows * k, "a"),
+        _row_scales(q, a_scale, dev, rows, k, "a_scale"), _arg(w, dev, 1, cfg.num_experts * n * k, "w"),
+        _weight_scales(cfg, w_scale, dev, n, k, "w_scale"), hp, _arg(y, dev, 2, rows * n, "y"),
+        _raw_stream(stream, dev))
+    if code:
+        raise MoeError("moe_expert_gemm", code)
 
 
 def moe_expert_gemm_swiglu(cfg: MoeConfig, num_tokens: int, inter: int, a: torch.Tensor, a_scale: torch.Tensor,
@@ -639,18 +653,23 @@ def moe_expert_gemm_swiglu(cfg: MoeConfig, num_tokens: int, inter: int, a: torch
                            h_scale: torch.Tensor, stream=None) -> None:
     """(h, h_scale)[row] = quantize(silu(gate) * up) with gate and up the two
     halves of a[row] @ w13[e].T."""
-    lib = _load()
     if cfg.quant == QUANT_NONE:
         raise MoeError("moe_expert_gemm_swiglu", MOE_ERR_UNSUPPORTED)
-    rows, H = _gemm_rows(cfg, num_tokens, handle), cfg.hidden
-    _one_device(stream, a=a, a_scale=a_scale, w13=w13, w13_scale=w13_scale, h=h, h_scale=h_scale,
-                handle=None if handle is None else handle.recv_count)
-    wp, wsp = _weight_ptrs(cfg, w13, w13_scale, 2 * inter, H, "w13")
-    _check("moe_expert_gemm_swiglu", lib.moe_expert_gemm_swiglu(
-        ctypes.byref(cfg), int(num_tokens), int(inter), _ptr(a, 1, rows * H, "a"),
-        _act_scale(cfg.quant, a_scale, rows, H, "a_scale"), wp, wsp,
-        None if handle is None else ctypes.byref(handle.c), _ptr(h, 1, rows * inter, "h"),
-        _act_scale(cfg.quant, h_scale, rows, inter, "h_scale"), _stream(stream)))
+    dev, q, H = _device(stream), cfg.quant, cfg.hidden
+    hp = None
+    rows = num_tokens
+    if handle is not None:
+        rows = moe_rows_capacity(cfg)
+        _arg(handle.recv_count, dev, 4, cfg.num_experts, "handle")
+        hp = ctypes.byref(handle.c)
+    code = _load().moe_expert_gemm_swiglu(
+        ctypes.byref(cfg), num_tokens, inter, _arg(a, dev, 1, rows * H, "a"),
+        _row_scales(q, a_scale, dev, rows, H, "a_scale"),
+        _arg(w13, dev, 1, cfg.num_experts * 2 * inter * H, "w13"),
+        _weight_scales(cfg, w13_scale, dev, 2 * inter, H, "w13_scale"), hp, _arg(h, dev, 1, rows * inter, "h"),
+        _row_scales(q, h_scale, dev, rows, inter, "h_scale"), _raw_stream(stream, dev))
+    if code:
+        raise MoeError("moe_expert_gemm_swiglu", code)
 
 
 def moe_layer_workspace_bytes(cfg: MoeConfig, inter: int) -> int:
@@ -663,14 +682,15 @@ def moe_layer_fused(cfg: MoeConfig, num_tokens: int, inter: int, topk_idx: torch
                     stream=None) -> None:
     """out[t] = sum_k topk_w[t,k] * W2[e] (silu(W13g[e] x[t]) * (W13u[e] x[t]))
     for at most LAYER_MAX_TOKENS tokens, in two kernels."""
-    lib = _load()
-    H, P = cfg.hidden, num_tokens * cfg.num_topk
-    _one_device(stream, topk_idx=topk_idx, topk_w=topk_w, x=x, w13=w13, w13_scale=w13_scale, w2=w2,
-                w2_scale=w2_scale, workspace=workspace, out=out)
-    w13p, w13s = _weight_ptrs(cfg, w13, w13_scale, 2 * inter, H, "w13")
-    w2p, w2s = _weight_ptrs(cfg, w2, w2_scale, H, inter, "w2")
-    _check("moe_layer_fused", lib.moe_layer_fused(
-        ctypes.byref(cfg), int(num_tokens), int(inter), _ptr(topk_idx, 4, P, "topk_idx"),
-        _ptr(topk_w, 4, P, "topk_w"), _ptr(x, 2, num_tokens * H, "x"), w13p, w13s, w2p, w2s,
-        _ptr(workspace, None, 0, "workspace"), workspace.numel() * workspace.element_size(),
-        _ptr(out, 2, num_tokens * H, "out"), _stream(stream)))
+    dev, H, P, E = _device(stream), cfg.hidden, num_tokens * cfg.num_topk, cfg.num_experts
+    elem = 2 if cfg.quant == QUANT_NONE else 1
+    ws_elem = workspace.element_size()
+    code = _load().moe_layer_fused(
+        ctypes.byref(cfg), num_tokens, inter, _arg(topk_idx, dev, 4, P, "topk_idx"),
+        _arg(topk_w, dev, 4, P, "topk_w"), _arg(x, dev, 2, num_tokens * H, "x"),
+        _arg(w13, dev, elem, E * 2 * inter * H, "w13"), _weight_scales(cfg, w13_scale, dev, 2 * inter, H, "w13_scale"),
+        _arg(w2, dev, elem, E * H * inter, "w2"), _weight_scales(cfg, w2_scale, dev, H, inter, "w2_scale"),
+        _arg(workspace, dev, ws_elem, 0, "workspace"), workspace.numel() * ws_elem,
+        _arg(out, dev, 2, num_tokens * H, "out"), _raw_stream(stream, dev))
+    if code:
+        raise MoeError("moe_layer_fused", code)

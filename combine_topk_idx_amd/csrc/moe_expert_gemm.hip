@@ -10,6 +10,8 @@
 // fp32 scales are applied to each block's result as it is added to the running
 // sum; power-of-two scales go into the matrix instruction (one byte per 32
 // channels of a lane's row) and the sum stays in its accumulator.
+#include <type_traits>
+
 #include "moe_mma.h"
 
 namespace moe {
@@ -21,14 +23,25 @@ constexpr int kGemmWaves = kGemmThreads / kWave;
 constexpr int kNF = 4;                        // 16-channel fragments per wave
 constexpr int kTileN = kGemmWaves * kNF * 16;  // output channels per block
 
+// A value that is the same in every lane, in a scalar register.  Where the
+// compiler can tell that it is, it drops a plain readfirstlane, may keep the
+// value in a vector register all the same (a quotient, threadIdx.x / 64) and
+// then turns each load through a descriptor that depends on it into a loop:
+// the empty asm hides what it can tell.
+__device__ __forceinline__ int32_t scalar(int32_t v)
+{
+    asm("" : "+v"(v));
+    return __builtin_amdgcn_readfirstlane(v);
+}
+
 // tile_start[e] = row tiles of BM rows before expert e; [E] = all.  Block-wide,
 // ends with a barrier.
-template <int BM>
+template <int BM, int NT>
 __device__ inline void scan_tiles(const int32_t *recv_count, int32_t E, int32_t dense_rows, int32_t *tile_start,
                                   int32_t *red)
 {
     const int tid = threadIdx.x, lane = tid & (kWave - 1), wave = tid / kWave;
-    const int per = (E + kGemmThreads - 1) / kGemmThreads;
+    const int per = (E + NT - 1) / NT;
     const int e0 = min(E, tid * per), e1 = min(E, e0 + per);
     int32_t local = 0;
     for (int e = e0; e < e1; ++e)
@@ -37,12 +50,12 @@ __device__ inline void scan_tiles(const int32_t *recv_count, int32_t E, int32_t 
     if (lane == kWave - 1)
         red[wave] = incl;
     __syncthreads();
-    int32_t run = dev::sum_before<kGemmWaves>(red, wave) + incl - local;
+    int32_t run = dev::sum_before<NT / kWave>(red, wave) + incl - local;
     for (int e = e0; e < e1; ++e) {
         tile_start[e] = run;
         run += ((recv_count != nullptr ? recv_count[e] : dense_rows) + BM - 1) / BM;
     }
-    if (tid == kGemmThreads - 1)
+    if (tid == NT - 1)
         tile_start[E] = run;
     __syncthreads();
 }
@@ -53,7 +66,7 @@ __device__ __forceinline__ int find_expert(const int32_t *tile_start, int32_t E,
     int lo = 0, hi = E;
     while (hi - lo > 1) {
         const int mid = (lo + hi) >> 1;
-        if (tile_start[mid] <= m)
+        if (scalar(tile_start[mid]) <= m)
             lo = mid;
         else
             hi = mid;
@@ -61,83 +74,95 @@ __device__ __forceinline__ int find_expert(const int32_t *tile_start, int32_t E,
     return lo;
 }
 
-// Writes a tile's results: bf16 outputs, or SwiGLU + quantization of the gate
-// (f < 2) and up fragments.  Block-wide with SWIGLU.
+// A tile of work: rows [row0, row0 + valid) of expert e, channel tile nt.
+struct TileAt {
+    int32_t e, nt, valid;
+    int64_t row0;
+    __device__ __forceinline__ TileAt scalars() const
+    {
+        const uint64_t lo = (uint32_t)scalar((int32_t)row0), hi = (uint32_t)scalar((int32_t)(row0 >> 32));
+        return TileAt{scalar(e), scalar(nt), scalar(valid), (int64_t)(hi << 32 | lo)};
+    }
+};
+
+// Writes a wave's results: rows 16 MT wr + 16 i + (lane % 16), channels n0[f] + 4
+// (lane / 16) + j.  bf16 outputs, or (SWIGLU; fragments f < 2 hold the gate,
+// f >= 2 the up products) SwiGLU and quantization, block-wide: the WC waves of
+// a row share its 128-channel block (each has one MX block of 32).
 template <int QUANT, int MT, bool SWIGLU, int BM>
-__device__ __forceinline__ void write_tile(const ExpertGemmArgs &p, dev::f32x4 (&acc)[kNF][MT],
-                                           const int32_t (&n0)[kNF], int64_t row0, int32_t valid, int32_t nt, int wave,
-                                           int lane, float (*wave_max)[BM])
+__device__ __forceinline__ void write_tile(const ExpertGemmArgs &p, dev::f32x4 (&acc)[kNF][MT], const TileAt &at,
+                                           int wr, int wc, int lane, float (*wave_max)[BM])
 {
     const int r = lane & 15, g = lane >> 4;
-            if constexpr (!SWIGLU) {
+    if constexpr (!SWIGLU) {
 #pragma unroll
-                for (int i = 0; i < MT; ++i) {
-                    const int32_t row = i * 16 + r;
+        for (int i = 0; i < MT; ++i) {
+            const int32_t row = (wr * MT + i) * 16 + r;
 #pragma unroll
-                    for (int f = 0; f < kNF; ++f) {
-                        const int32_t n = n0[f] + g * 4;
-                        if (row < valid && n < p.n)
-                            *reinterpret_cast<uint2 *>(p.y + (row0 + row) * p.n + n) =
-                                make_uint2(dev::pack_bf16(acc[f][i][0], acc[f][i][1]),
-                                           dev::pack_bf16(acc[f][i][2], acc[f][i][3]));
-                    }
+            for (int f = 0; f < kNF; ++f) {
+                const int32_t n = at.nt * kTileN + wc * 64 + f * 16 + g * 4;
+                if (row < at.valid && n < p.n)
+                    *reinterpret_cast<uint2 *>(p.y + (at.row0 + row) * p.n + n) =
+                        make_uint2(dev::pack_bf16(acc[f][i][0], acc[f][i][1]),
+                                   dev::pack_bf16(acc[f][i][2], acc[f][i][3]));
+            }
+        }
+    } else {
+        const int32_t inter = p.n / 2;
+        // h in the place of the gate accumulators; largest magnitude per row and wave
+#pragma unroll
+        for (int i = 0; i < MT; ++i) {
+            float amax = 0.0f;
+#pragma unroll
+            for (int f = 0; f < 2; ++f)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    acc[f][i][j] = dev::swiglu(acc[f][i][j], acc[f + 2][i][j]);
+                    amax = fmaxf(amax, fabsf(acc[f][i][j]));
                 }
-            } else {
-                const int32_t inter = p.n / 2;
-                // h in the place of the gate accumulators; largest magnitude per row and wave
+            amax = fmaxf(amax, __shfl_xor(amax, 16));
+            amax = fmaxf(amax, __shfl_xor(amax, 32));
+            if (g == 0)
+                wave_max[wc][(wr * MT + i) * 16 + r] = amax;
+        }
+        __syncthreads();
 #pragma unroll
-                for (int i = 0; i < MT; ++i) {
-                    float amax = 0.0f;
+        for (int i = 0; i < MT; ++i) {
+            const int32_t row = (wr * MT + i) * 16 + r;
+            float amax = wave_max[wc][row];
+            if constexpr (QUANT != MOE_QUANT_MXFP8) {
 #pragma unroll
-                    for (int f = 0; f < 2; ++f)
+                for (int w = 0; w < 4; ++w)
+                    amax = fmaxf(amax, wave_max[w][row]);
+            }
+            const dev::BlockScale<QUANT> bs(amax);
+            if (row < at.valid) {
+                const int64_t grow = at.row0 + row;
 #pragma unroll
-                        for (int j = 0; j < 4; ++j) {
-                            acc[f][i][j] = dev::swiglu(acc[f][i][j], acc[f + 2][i][j]);
-                            amax = fmaxf(amax, fabsf(acc[f][i][j]));
-                        }
-                    amax = fmaxf(amax, __shfl_xor(amax, 16));
-                    amax = fmaxf(amax, __shfl_xor(amax, 32));
+                for (int f = 0; f < 2; ++f)
+                    *reinterpret_cast<uint32_t *>(p.h + grow * inter + at.nt * 128 + wc * 32 + f * 16 + g * 4) =
+                        dev::pack_e4m3(bs.apply(acc[f][i][0]), bs.apply(acc[f][i][1]), bs.apply(acc[f][i][2]),
+                                       bs.apply(acc[f][i][3]));
+                const int HB = inter / kQuantGroup;
+                if constexpr (QUANT == MOE_QUANT_FP8_F32) {
+                    if (wc == 0 && g == 0)
+                        static_cast<float *>(p.h_scale)[grow * HB + at.nt] = bs.s;
+                } else if constexpr (QUANT == MOE_QUANT_FP8_UE8M0) {
+                    const int HW = (HB + 3) / 4 * 4;
+                    uint8_t *sc = static_cast<uint8_t *>(p.h_scale) + grow * HW;
+                    if (wc == 0 && g == 0) {
+                        sc[at.nt] = (uint8_t)bs.byte;
+                        if (at.nt == HB - 1)  // the last word's unused high bytes are 0
+                            for (int b = HB; b < HW; ++b)
+                                sc[b] = 0;
+                    }
+                } else {
                     if (g == 0)
-                        wave_max[wave][i * 16 + r] = amax;
+                        static_cast<uint8_t *>(p.h_scale)[grow * HB * 4 + at.nt * 4 + wc] = (uint8_t)bs.byte;
                 }
-                __syncthreads();
-#pragma unroll
-                for (int i = 0; i < MT; ++i) {
-                    const int32_t row = i * 16 + r;
-                    float amax = wave_max[wave][row];
-                    if constexpr (QUANT != MOE_QUANT_MXFP8) {
-#pragma unroll
-                        for (int w = 0; w < kGemmWaves; ++w)
-                            amax = fmaxf(amax, wave_max[w][row]);
-                    }
-                    const dev::BlockScale<QUANT> bs(amax);
-                    if (row < valid) {
-                        const int64_t grow = row0 + row;
-#pragma unroll
-                        for (int f = 0; f < 2; ++f)
-                            *reinterpret_cast<uint32_t *>(p.h + grow * inter + n0[f] + g * 4) =
-                                dev::pack_e4m3(bs.apply(acc[f][i][0]), bs.apply(acc[f][i][1]), bs.apply(acc[f][i][2]),
-                                               bs.apply(acc[f][i][3]));
-                        const int HB = inter / kQuantGroup;
-                        if constexpr (QUANT == MOE_QUANT_FP8_F32) {
-                            if (wave == 0 && g == 0)
-                                static_cast<float *>(p.h_scale)[grow * HB + nt] = bs.s;
-                        } else if constexpr (QUANT == MOE_QUANT_FP8_UE8M0) {
-                            const int HW = (HB + 3) / 4 * 4;
-                            uint8_t *sc = static_cast<uint8_t *>(p.h_scale) + grow * HW;
-                            if (wave == 0 && g == 0) {
-                                sc[nt] = (uint8_t)bs.byte;
-                                if (nt == HB - 1)  // the last word's unused high bytes are 0
-                                    for (int b = HB; b < HW; ++b)
-                                        sc[b] = 0;
-                            }
-                        } else {
-                            if (g == 0)
-                                static_cast<uint8_t *>(p.h_scale)[grow * HB * 4 + nt * 4 + wave] = (uint8_t)bs.byte;
-                        }
-                    }
-                }
-                        }
+            }
+        }
+    }
 }
 
 template <int QUANT, int MT, bool SWIGLU>
@@ -153,7 +178,7 @@ __global__ __launch_bounds__(kGemmThreads) void expert_gemm_kernel(ExpertGemmArg
     const int r = lane & 15, g = lane >> 4;
     const int KB = p.k / kQuantGroup;
     const int KW = (KB + 3) / 4;
-    scan_tiles<BM>(p.recv_count, p.E, p.dense_rows, tile_start, red);
+    scan_tiles<BM, kGemmThreads>(p.recv_count, p.E, p.dense_rows, tile_start, red);
     const int64_t n_work = (int64_t)tile_start[p.E] * n_tiles;
 
     for (int64_t work = blockIdx.x; work < n_work; work += gridDim.x) {
@@ -233,268 +258,359 @@ __global__ __launch_bounds__(kGemmThreads) void expert_gemm_kernel(ExpertGemmArg
             }
         }
 
-        write_tile<QUANT, MT, SWIGLU>(p, acc, n0, row0, valid, nt, wave, lane, wave_max);
+        write_tile<QUANT, MT, SWIGLU, BM>(p, acc, TileAt{e, nt, valid, row0}, 0, wave, lane, wave_max);
+        __syncthreads();  // wave_max is rewritten by the next tile
     }
 }
 
 // ---------------------------------------------------------------------------
-// Large row groups: MT * 16 rows x 256 channels per block.
+// Large row groups: BM rows x 256 channels per block of 8 waves.
 //
-// Each of the four waves owns 64 channels and all the tile's rows, so a weight
-// byte goes from memory to the registers of the one wave that multiplies it,
-// one block of 128 channels ahead of its use, and only the rows -- which all
-// four waves read -- pass through LDS (double buffered, one barrier per block).
+// Rows, weights and scales of one 128-channel block form a stage, which loads
+// straight from memory into LDS (no registers in between); NS stages are in
+// turn, so NS - 1 blocks are in flight while one is multiplied.  A wave waits
+// for its own loads of a stage, a barrier makes the others' visible, and the
+// stage that was multiplied before the barrier takes the next block.  Blocks
+// are persistent: the first stages of a block's next tile load while it
+// writes its last one's results.
 // ---------------------------------------------------------------------------
 
+constexpr int kTileThreads = 512;
+constexpr int kTileWaves = kTileThreads / kWave;
 constexpr int kMGroup = 8;   // row tiles that walk the channel tiles together
-
-// (a condition inside the block loop would split it, and the compiler then moves
-// the matrix instructions past the barrier)
-template <int QUANT, int BM>
-struct TileLds {
-    alignas(16) uint8_t rows[2][BM * kQuantGroup];
-    uint32_t sa[2][kGemmThreads];   // scale word of each row (a slot per thread: stores need no condition)
-    uint32_t sw[2][kGemmThreads];   // and of the weights' channels (MXFP8) or blocks (the first two)
-};
-
-// A tile of work: rows [row0, row0 + valid) of expert e, channel tile nt.
-struct TileAt {
-    int32_t e, nt, valid;
-    int64_t row0;
-};
+constexpr int kWaveRows = 2, kWaveCols = 4;  // waves over the tile's rows and channels
 
 // Buffer descriptor over `bytes` bytes (loads past them return 0), the same in
 // every lane.
 __device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer(const void *p, uint32_t bytes)
 {
     const uint64_t a = (uint64_t)p;
-    const uint64_t lo = (uint32_t)__builtin_amdgcn_readfirstlane((uint32_t)a);
-    const uint64_t hi = (uint32_t)__builtin_amdgcn_readfirstlane((uint32_t)(a >> 32));
-    return __builtin_amdgcn_make_buffer_rsrc((void *)(hi << 32 | lo), 0, __builtin_amdgcn_readfirstlane(bytes),
+    const uint64_t lo = (uint32_t)scalar((int32_t)a);
+    const uint64_t hi = (uint32_t)scalar((int32_t)(a >> 32));
+    return __builtin_amdgcn_make_buffer_rsrc((void *)(hi << 32 | lo), 0, scalar((int32_t)bytes),
                                              0x00020000);
-}
-__device__ __forceinline__ dev::u32x4 load16(__amdgpu_buffer_rsrc_t b, uint32_t voff, uint32_t soff)
-{
-    return __builtin_bit_cast(dev::u32x4, __builtin_amdgcn_raw_buffer_load_b128(b, voff, soff, 0));
 }
 __device__ __forceinline__ dev::i32x8 join(const dev::u32x4 &l, const dev::u32x4 &h)
 {
     return dev::i32x8{(int)l[0], (int)l[1], (int)l[2], (int)l[3], (int)h[0], (int)h[1], (int)h[2], (int)h[3]};
 }
 
-template <int QUANT, int BM, bool SWIGLU, int MT>
-__device__ __forceinline__ void run_tile(const ExpertGemmArgs &p, const TileAt &at, TileLds<QUANT, BM> &lds,
-                                         float (*wave_max)[BM])
+// Memory -> LDS: BYTES per lane, lane l to dst + l * BYTES.
+template <int BYTES>
+__device__ __forceinline__ void load_lds(__amdgpu_buffer_rsrc_t b, uint8_t *dst, uint32_t voff, uint32_t soff)
 {
-    constexpr int kRows = MT * 16;
-    constexpr int kStage = kRows * 8 / kGemmThreads;  // 16-byte pieces per thread and block
-    constexpr int GR = 1;                             // row fragments read together
-    static_assert(MT >= 2 && MT % GR == 0 && kRows <= kGemmThreads, "staging covers whole row groups");
-    const int tid = threadIdx.x;
-    const int lane = tid & (kWave - 1);
-    const int wave = __builtin_amdgcn_readfirstlane(tid / kWave);
-    const int r = lane & 15, g = lane >> 4;
-    const uint32_t k = (uint32_t)p.k;
-    const int KB = p.k / kQuantGroup;
-    const int SW = QUANT == MOE_QUANT_FP8_UE8M0 ? (KB + 3) / 4 : KB;  // scale words of a row
-    const int NBn = (p.n + kQuantGroup - 1) / kQuantGroup;
-
-    // rows: piece tid % 8 of row tid / 8 + 32 j; rows past the segment read as 0
-    const __amdgpu_buffer_rsrc_t abuf = buffer(p.a + at.row0 * p.k, (uint32_t)at.valid * k);
-    const uint32_t avo = (uint32_t)(tid >> 3) * k + (tid & 7) * 16;
-    // their scale words: row tid
-    const __amdgpu_buffer_rsrc_t sabuf =
-        buffer(static_cast<const uint32_t *>(p.a_scale) + at.row0 * SW, (uint32_t)at.valid * SW * 4);
-    const uint32_t savo = (uint32_t)tid * SW * 4;
-    // weights: 64 channels of this wave (SwiGLU: 32 of the gate, 32 of the up half)
-    int32_t n0[kNF];
-    __amdgpu_buffer_rsrc_t wbuf[2];
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-        const int32_t c = SWIGLU ? at.nt * 128 + wave * 32 + h * (p.n / 2) : at.nt * kTileN + wave * 64 + h * 32;
-        n0[2 * h] = c;
-        n0[2 * h + 1] = c + 16;
-        const int32_t left = max(0, min(32, p.n - c));
-        wbuf[h] = buffer(p.w + ((int64_t)at.e * p.n + min(c, p.n - 1)) * p.k, (uint32_t)left * k);
-    }
-    const uint32_t wvo = (uint32_t)r * k + 16 * g;
-    // their scale words: MXFP8 one per channel (channel tid of the tile), else
-    // one per 128-channel block (threads 0 and 1)
-    uint32_t sw_row;
-    if constexpr (QUANT == MOE_QUANT_MXFP8)
-        sw_row = SWIGLU ? at.nt * 128 + (tid & 127) + (tid >> 7) * (p.n / 2) : min(at.nt * kTileN + tid, p.n - 1);
+    auto *to = (__attribute__((address_space(3))) void *)dst;
+    if constexpr (BYTES == 16)
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(b, to, 16, voff, soff, 0, 0);
     else
-        sw_row = SWIGLU ? at.nt + (tid & 1) * (NBn / 2) : min(at.nt * 2 + (tid & 1), NBn - 1);
-    const uint32_t sw_rows = QUANT == MOE_QUANT_MXFP8 ? p.n : NBn;
-    const __amdgpu_buffer_rsrc_t swbuf =
-        buffer(static_cast<const uint32_t *>(p.w_scale) + (int64_t)at.e * sw_rows * SW, sw_rows * SW * 4);
-    const uint32_t swvo = sw_row * SW * 4;
-    // 16-byte piece c of a row sits at position c ^ ((row >> 1) & 7) in LDS: the
-    // 16 rows of a fragment then cover all banks
-    const int spos = (tid >> 3) * kQuantGroup + (((tid & 7) ^ ((tid >> 4) & 7)) * 16);
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(b, to, 4, voff, soff, 0, 0);
+}
+
+// Waits until at most `vm` of this wave's memory loads are outstanding and all
+// of its LDS reads are done, then for the block's other waves.
+template <int VM>
+__device__ __forceinline__ void wait_and_meet()
+{
+    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(VM) : "memory");
+}
+
+// f(0), f(1), .. f(N - 1) with the number as a type.
+template <int N, typename F>
+__device__ __forceinline__ void for_each(const F &f)
+{
+    if constexpr (N > 0) {
+        for_each<N - 1>(f);
+        f(std::integral_constant<int, N - 1>());
+    }
+}
+
+// One stage in LDS: rows, weights, then scale words, 64 per wave: one per row,
+// then one per channel (MXFP8) or 128-channel block (the first two).
+template <int BM>
+struct Stage {
+    static constexpr int kW = BM * kQuantGroup;
+    static constexpr int kSa = kW + kTileN * kQuantGroup;
+    static constexpr int kSw = kSa + BM * 4;
+    static constexpr int kBytes = kSa + kTileWaves * kWave * 4;
+    static constexpr int kLoads = BM / 64 + 4 + 1;  // loads of a wave per stage
+};
+
+// The loads of one tile: descriptors (uniform) and this lane's offsets.
+// Rows past the tile's end are read as its last row and channels past the last
+// as that one: every address is inside its array, and what comes of the
+// copies is not stored.  The descriptors' range check serves one purpose, the
+// blocks after the last one (bit 31 of a lane's offset, see issue); it compares
+// the lane's offset with num_records minus the scalar offset, so the scalar
+// offset always stays below num_records.
+template <int QUANT, bool SWIGLU, int BM>
+struct TileLoads {
+    __amdgpu_buffer_rsrc_t a, w[2], s;
+    uint32_t ao[BM / 64], wo[SWIGLU ? 2 : 4], so;  // rows, weights (both halves alike with SWIGLU), scales
+    int KB, wave, rot;
+
+    // Tiles start their walk over the blocks at different ones: rows lie k bytes
+    // apart, so tiles in step would all read the same few channels of L2.
+    __device__ __forceinline__ int block(int kb) const { return kb + rot < KB ? kb + rot : kb + rot - KB; }
+
+    __device__ __forceinline__ void set(const ExpertGemmArgs &p, const TileAt &at, int wave_, int lane)
+    {
+        wave = wave_;
+        const uint32_t k = (uint32_t)p.k;
+        KB = p.k / kQuantGroup;
+        rot = 0;
+        const int SW = QUANT == MOE_QUANT_FP8_UE8M0 ? (KB + 3) / 4 : KB;  // scale words of a row
+        const int NBn = (p.n + kQuantGroup - 1) / kQuantGroup;
+        // 16-byte piece c of a row sits at position c ^ ((row >> 1) & 7) in LDS:
+        // the 16 rows of a fragment then cover all banks.  A wave loads rows 8 j
+        // .. 8 j + 7, j = wave (mod 8): lane l holds position l % 8 of row l / 8.
+        const uint32_t piece = ((lane & 7) ^ ((4 * (wave & 1) + (lane >> 4)) & 7)) * 16;
+        const int row = 8 * wave + (lane >> 3);
+        a = buffer(p.a + at.row0 * p.k, (uint32_t)at.valid * k);
+#pragma unroll
+        for (int i = 0; i < BM / 64; ++i)
+            ao[i] = (uint32_t)min(row + 64 * i, at.valid - 1) * k + piece;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int32_t c = min(SWIGLU ? at.nt * 128 + h * (p.n / 2) : at.nt * kTileN + h * 128, p.n - 1);
+            const int32_t left = min(128, p.n - c);
+            w[h] = buffer(p.w + ((int64_t)at.e * p.n + c) * p.k, (uint32_t)left * k);
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+                wo[SWIGLU ? i : 2 * h + i] = (uint32_t)min(row + 64 * i, left - 1) * k + piece;
+        }
+        // scales: the first BM / 64 waves load the rows' words, the others the weights'
+        static_assert(QUANT != MOE_QUANT_MXFP8 || BM <= 256, "MXFP8 needs four waves for the channels' words");
+        const bool of_rows = wave < BM / kWave;
+        const int t = (of_rows ? wave : wave - BM / kWave) * kWave + lane;
+        const int32_t w_rows = QUANT == MOE_QUANT_MXFP8 ? p.n : NBn;
+        const int32_t w_row = QUANT == MOE_QUANT_MXFP8
+                                  ? (SWIGLU ? at.nt * 128 + (t & 127) + (t >> 7) * (p.n / 2) : at.nt * kTileN + t)
+                                  : (SWIGLU ? at.nt + (t & 1) * (NBn / 2) : at.nt * 2 + (t & 1));
+        const void *src = of_rows ? p.a_scale : p.w_scale;
+        const int64_t first = of_rows ? at.row0 : (int64_t)at.e * w_rows;
+        const int32_t rows = of_rows ? at.valid : w_rows;
+        s = buffer(static_cast<const uint32_t *>(src) + first * SW, (uint32_t)rows * SW * 4);
+        so = (uint32_t)min(of_rows ? t : w_row, rows - 1) * SW * 4;
+    }
+    // Loads FROM .. TO - 1 of block kb into a stage; the blocks after the last
+    // are asked for past the buffers' ends, which costs no memory access.
+    template <int FROM, int TO>
+    __device__ __forceinline__ void issue(uint8_t *st, int kb) const
+    {
+        constexpr int kA = BM / 64;
+        const uint32_t past = kb < KB ? 0u : 0x80000000u;
+        const int b = kb < KB ? block(kb) : 0;
+        const uint32_t at_k = (uint32_t)b * kQuantGroup;
+#pragma unroll
+        for (int j = FROM; j < TO; ++j) {
+            if (j < kA) {
+                load_lds<16>(a, st + (wave + 8 * j) * 1024, ao[j] | past, at_k);
+            } else if (j < kA + 4) {
+                const int i = j - kA;
+                load_lds<16>(w[i >> 1], st + Stage<BM>::kW + (wave + 8 * i) * 1024, wo[SWIGLU ? i & 1 : i] | past,
+                             at_k);
+            } else {
+                const uint32_t word = QUANT == MOE_QUANT_FP8_UE8M0 ? (uint32_t)b >> 2 : (uint32_t)b;
+                load_lds<4>(s, st + Stage<BM>::kSa + wave * 256, so | past, word * 4);
+            }
+        }
+    }
+};
+
+// acc += the stage's block for this wave's MT row fragments and kNF channel
+// fragments, while block `kb_load` loads into the stage `free`: its loads are
+// spread over the matrix instructions (all at once they would hold up the
+// wave's LDS reads until the address unit has taken them).
+template <int QUANT, bool SWIGLU, int BM, int MT>
+__device__ __forceinline__ void multiply_stage(dev::f32x4 (&acc)[kNF][MT], const uint8_t *st, int wr, int wc, int lane,
+                                               int u, const TileLoads<QUANT, SWIGLU, BM> &loads, uint8_t *free,
+                                               int kb_load)
+{
+    constexpr int kLoads = Stage<BM>::kLoads;
+    const int r = lane & 15, g = lane >> 4;
     const int rswz = (r >> 1) & 7;
     const int rlo = r * kQuantGroup + ((g ^ rswz) * 16), rhi = r * kQuantGroup + (((4 + g) ^ rswz) * 16);
+    const uint8_t *rows = st + wr * MT * 16 * kQuantGroup;
+    const uint32_t *sa = reinterpret_cast<const uint32_t *>(st + Stage<BM>::kSa) + wr * MT * 16 + r;
+    const uint32_t *sw = reinterpret_cast<const uint32_t *>(st + Stage<BM>::kSw);
+    dev::i32x8 w[kNF], x[2];
+    uint32_t sx[2];
+    int swb[kNF];
+    float swf[2];
+    const auto read_row = [&](int i) {
+        x[i & 1] = join(*reinterpret_cast<const dev::u32x4 *>(rows + rlo + i * 16 * kQuantGroup),
+                        *reinterpret_cast<const dev::u32x4 *>(rows + rhi + i * 16 * kQuantGroup));
+        sx[i & 1] = sa[i * 16];
+    };
+#pragma unroll
+    for (int f = 0; f < kNF; ++f) {
+        const int c = SWIGLU ? wc * 32 + (f & 1) * 16 + (f >> 1) * 128 : wc * 64 + f * 16;
+        const uint8_t *src = st + Stage<BM>::kW + c * kQuantGroup;
+        w[f] = join(*reinterpret_cast<const dev::u32x4 *>(src + rlo), *reinterpret_cast<const dev::u32x4 *>(src + rhi));
+        if constexpr (QUANT == MOE_QUANT_MXFP8)
+            swb[f] = (int)(sw[c + r] >> (8 * g));
+        if (f == 0)
+            read_row(0);
+    }
+    if constexpr (QUANT == MOE_QUANT_FP8_F32) {
+        swf[0] = __uint_as_float(sw[SWIGLU ? 0 : wc >> 1]);
+        swf[1] = SWIGLU ? __uint_as_float(sw[1]) : swf[0];
+    } else if constexpr (QUANT == MOE_QUANT_FP8_UE8M0) {
+        swb[0] = swb[1] = (int)(sw[SWIGLU ? 0 : wc >> 1] >> (8 * u));
+        swb[2] = swb[3] = SWIGLU ? (int)(sw[1] >> (8 * u)) : swb[0];
+    }
+    const auto part = [&](auto I) {
+        constexpr int i = decltype(I)::value;
+        if constexpr (i + 1 < MT)
+            read_row(i + 1);
+        if constexpr (QUANT == MOE_QUANT_FP8_F32) {
+            const float s0 = __uint_as_float(sx[i & 1]) * swf[0];
+            const float s1 = SWIGLU ? __uint_as_float(sx[i & 1]) * swf[1] : s0;
+            dev::f32x4 d[kNF];
+#pragma unroll
+            for (int f = 0; f < kNF; ++f) {
+                const dev::f32x4 z = {0.0f, 0.0f, 0.0f, 0.0f};
+                d[f] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(w[f], x[i & 1], z, 0, 0, 0, 0, 0, 0);
+            }
+            loads.template issue<i * kLoads / MT, (i + 1) * kLoads / MT>(free, kb_load);
+#pragma unroll
+            for (int f = 0; f < kNF; ++f)
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    acc[f][i][j] = __builtin_fmaf(d[f][j], f < 2 ? s0 : s1, acc[f][i][j]);
+        } else {
+            const int sb = (int)(sx[i & 1] >> (8 * (QUANT == MOE_QUANT_FP8_UE8M0 ? u : g)));
+#pragma unroll
+            for (int f = 0; f < kNF; ++f)
+                acc[f][i] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(w[f], x[i & 1], acc[f][i], 0, 0, 0,
+                                                                              swb[f], 0, sb);
+            loads.template issue<i * kLoads / MT, (i + 1) * kLoads / MT>(free, kb_load);
+        }
+        __builtin_amdgcn_sched_barrier(0);
+    };
+    for_each<MT>(part);
+}
 
+// Starts the loads of a tile's first NS - 1 stages.
+template <int QUANT, bool SWIGLU, int BM, int NS>
+__device__ __forceinline__ void start_tile(const ExpertGemmArgs &p, const TileAt &at, uint8_t *st0, uint8_t *st1,
+                                           int wave, int lane)
+{
+    TileLoads<QUANT, SWIGLU, BM> loads;
+    loads.set(p, at, wave, lane);
+    loads.template issue<0, Stage<BM>::kLoads>(st0, 0);
+    if constexpr (NS == 3)
+        loads.template issue<0, Stage<BM>::kLoads>(st1, 1);
+}
+
+// Multiplies a tile whose first NS - 1 stages are in flight, then starts the
+// next tile's (`more`) and writes the results.
+template <int QUANT, bool SWIGLU, int BM, int NS, int MT>
+__device__ __forceinline__ void run_tile(const ExpertGemmArgs &p, const TileAt &at, const TileAt &next, bool more,
+                                         uint8_t *st0, uint8_t *st1, uint8_t *st2, int wave, int lane)
+{
+    TileLoads<QUANT, SWIGLU, BM> loads;
+    loads.set(p, at, wave, lane);
+    constexpr int kAhead = Stage<BM>::kLoads * (NS - 2);
+    const int wr = wave / kWaveCols, wc = wave % kWaveCols;
+    const int KB = loads.KB;
     dev::f32x4 acc[kNF][MT];
 #pragma unroll
     for (int f = 0; f < kNF; ++f)
 #pragma unroll
         for (int i = 0; i < MT; ++i)
             acc[f][i] = dev::f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-
-    dev::u32x4 xr[kStage];
-    uint32_t sav, swv;
-    dev::u32x4 wf[2][2 * kNF];
-    // All loads of block kb.  The block after the last one is asked for as an
-    // address past every buffer's end, which costs no memory access.
-    const auto load = [&](dev::u32x4(&w)[2 * kNF], int kb) {
-        const uint32_t past = kb < KB ? 0u : 0x80000000u;
-        const uint32_t at_k = (uint32_t)kb * kQuantGroup | past;
-        const int word = QUANT == MOE_QUANT_FP8_UE8M0 ? min(kb, KB - 1) >> 2 : min(kb, KB - 1);
-#pragma unroll
-        for (int j = 0; j < kStage; ++j)
-            xr[j] = load16(abuf, avo, (uint32_t)(32 * j) * k + at_k);
-        sav = __builtin_amdgcn_raw_buffer_load_b32(sabuf, savo, word * 4, 0);
-        swv = __builtin_amdgcn_raw_buffer_load_b32(swbuf, swvo, word * 4, 0);
-#pragma unroll
-        for (int f = 0; f < kNF; ++f) {
-            const uint32_t so = (uint32_t)(16 * (f & 1)) * k + at_k;
-            w[2 * f] = load16(wbuf[f >> 1], wvo, so);
-            w[2 * f + 1] = load16(wbuf[f >> 1], wvo + 64, so);
-        }
+    const auto step = [&](uint8_t *cur, uint8_t *free, int kb) {
+        wait_and_meet<kAhead>();
+        multiply_stage<QUANT, SWIGLU, BM, MT>(acc, cur, wr, wc, lane, loads.block(kb) & 3, loads, free, kb + NS - 1);
     };
-    // Rows and scales of the loaded block, into LDS buffer `buf`.
-    const auto store = [&](int buf) {
-#pragma unroll
-        for (int j = 0; j < kStage; ++j)
-            *reinterpret_cast<dev::u32x4 *>(&lds.rows[buf][spos + 32 * j * kQuantGroup]) = xr[j];
-        lds.sa[buf][tid] = sav;
-        lds.sw[buf][tid] = swv;
-    };
-    // One block of 128 channels: GR row fragments at a time, the next ones read
-    // from LDS while these are multiplied.
-    const auto multiply = [&](const dev::u32x4(&w)[2 * kNF], int buf, int u) {
-        float swf[2] = {};
-        int swb[kNF] = {};
-        if constexpr (QUANT == MOE_QUANT_FP8_F32) {
-            swf[0] = __uint_as_float(lds.sw[buf][SWIGLU ? 0 : wave >> 1]);
-            swf[1] = SWIGLU ? __uint_as_float(lds.sw[buf][1]) : swf[0];
-        } else if constexpr (QUANT == MOE_QUANT_FP8_UE8M0) {
-            swb[0] = swb[1] = (int)(lds.sw[buf][SWIGLU ? 0 : wave >> 1] >> (8 * u));
-            swb[2] = swb[3] = SWIGLU ? (int)(lds.sw[buf][1] >> (8 * u)) : swb[0];
-        } else {
-#pragma unroll
-            for (int f = 0; f < kNF; ++f) {
-                const int n = SWIGLU ? wave * 32 + (f & 1) * 16 + (f >> 1) * 128 + r : wave * 64 + f * 16 + r;
-                swb[f] = (int)(lds.sw[buf][n] >> (8 * g));
-            }
+    int kb = 0;
+    if constexpr (NS == 3) {
+        for (; kb + 3 <= KB; kb += 3) {
+            step(st0, st2, kb);
+            step(st1, st0, kb + 1);
+            step(st2, st1, kb + 2);
         }
-        const uint8_t *rows = lds.rows[buf];
-        dev::u32x4 lo[2][GR], hi[2][GR];
-        uint32_t sv[2][GR];
-        const auto read = [&](int b, int i0) {
-#pragma unroll
-            for (int i = 0; i < GR; ++i) {
-                lo[b][i] = *reinterpret_cast<const dev::u32x4 *>(rows + rlo + (i0 + i) * 16 * kQuantGroup);
-                hi[b][i] = *reinterpret_cast<const dev::u32x4 *>(rows + rhi + (i0 + i) * 16 * kQuantGroup);
-                sv[b][i] = lds.sa[buf][(i0 + i) * 16 + r];
-            }
-        };
-        read(0, 0);
-#pragma unroll
-        for (int c = 0; c < MT / GR; ++c) {
-            if (c + 1 < MT / GR)
-                read((c + 1) & 1, (c + 1) * GR);
-            __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-            for (int i = 0; i < GR; ++i) {
-                const dev::i32x8 x = join(lo[c & 1][i], hi[c & 1][i]);
-                const uint32_t s = sv[c & 1][i];
-                if constexpr (QUANT == MOE_QUANT_FP8_F32) {
-                    const float s0 = __uint_as_float(s) * swf[0];
-                    const float s1 = SWIGLU ? __uint_as_float(s) * swf[1] : s0;
-#pragma unroll
-                    for (int f = 0; f < kNF; ++f) {
-                        const dev::f32x4 z = {0.0f, 0.0f, 0.0f, 0.0f};
-                        const dev::f32x4 d = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
-                            join(w[2 * f], w[2 * f + 1]), x, z, 0, 0, 0, 0, 0, 0);
-#pragma unroll
-                        for (int j = 0; j < 4; ++j)
-                            acc[f][c * GR + i][j] = __builtin_fmaf(d[j], f < 2 ? s0 : s1, acc[f][c * GR + i][j]);
-                    }
-                } else {
-                    const int sb = (int)(s >> (8 * (QUANT == MOE_QUANT_FP8_UE8M0 ? u : g)));
-#pragma unroll
-                    for (int f = 0; f < kNF; ++f)
-                        acc[f][c * GR + i] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
-                            join(w[2 * f], w[2 * f + 1]), x, acc[f][c * GR + i], 0, 0, 0, swb[f], 0, sb);
-                }
-            }
+        if (kb < KB)
+            step(st0, st2, kb);
+        if (kb + 1 < KB)
+            step(st1, st0, kb + 1);
+    } else {
+        for (; kb + 2 <= KB; kb += 2) {
+            step(st0, st1, kb);
+            step(st1, st0, kb + 1);
         }
-    };
-
-    load(wf[0], 0);
-    store(0);
-    __syncthreads();
-    for (int kb = 0; kb < KB; kb += 2) {
-        load(wf[1], kb + 1);
-        __builtin_amdgcn_sched_barrier(0);
-        multiply(wf[0], 0, kb & 3);
-        store(1);
-        __syncthreads();
-        load(wf[0], kb + 2);
-        __builtin_amdgcn_sched_barrier(0);
-        // an odd block count ends with a block of zeros
-        multiply(wf[1], 1, (kb + 1) & 3);
-        store(0);
-        __syncthreads();
+        if (kb < KB)
+            step(st0, st1, kb);
     }
-    write_tile<QUANT, MT, SWIGLU>(p, acc, n0, at.row0, at.valid, at.nt, wave, lane, wave_max);
+    wait_and_meet<0>();
+    if (more)
+        start_tile<QUANT, SWIGLU, BM, NS>(p, next.scalars(), st0, st1, wave, lane);
+    // the stage that the next tile's loads leave alone holds the rows' maxima
+    write_tile<QUANT, MT, SWIGLU, BM>(p, acc, at, wr, wc, lane, reinterpret_cast<float(*)[BM]>(NS == 3 ? st2 : st1));
 }
 
-template <int QUANT, bool SWIGLU, int MT, int OCC>
-__global__ __launch_bounds__(kGemmThreads, OCC) void expert_gemm_tiles(ExpertGemmArgs p, int32_t n_tiles)
+template <int QUANT, bool SWIGLU, int BM, int NS>
+__global__ __launch_bounds__(kTileThreads) void expert_gemm_tiles(ExpertGemmArgs p, int32_t n_tiles)
 {
-    constexpr int BM = MT * 16;
     __shared__ int32_t tile_start[kMaxExperts + 1];
-    __shared__ int32_t red[kGemmWaves];
-    __shared__ float wave_max[kGemmWaves][BM];
-    __shared__ TileLds<QUANT, BM> lds;
-    scan_tiles<BM>(p.recv_count, p.E, p.dense_rows, tile_start, red);
-    const int64_t n_work = (int64_t)__builtin_amdgcn_readfirstlane(tile_start[p.E]) * n_tiles;
+    __shared__ int32_t red[kTileWaves];
+    // separate variables: the compiler then knows which reads follow which loads
+    __shared__ alignas(1024) uint8_t st0[Stage<BM>::kBytes];
+    __shared__ alignas(1024) uint8_t st1[Stage<BM>::kBytes];
+    __shared__ alignas(1024) uint8_t st2[NS == 3 ? Stage<BM>::kBytes : 16];
+    const int lane = threadIdx.x & (kWave - 1);
+    const int wave = scalar(threadIdx.x / kWave);
+    scan_tiles<BM, kTileThreads>(p.recv_count, p.E, p.dense_rows, tile_start, red);
+    const int64_t n_work = (int64_t)scalar(tile_start[p.E]) * n_tiles;
     // workgroups go to the 8 XCDs in turn: each XCD takes a contiguous run of
     // the work, so that the tiles of one expert share its L2
     const int64_t run = (n_work + 7) / 8;
+    const int64_t base = (int64_t)(blockIdx.x & 7) * run;
+    const int64_t end = min(run, n_work - base);
 
-    for (int64_t idx = blockIdx.x >> 3; idx < run; idx += gridDim.x >> 3) {
-        const int64_t work = (int64_t)(blockIdx.x & 7) * run + idx;
-        if (work >= n_work)
-            break;
-        // tiles of an expert: groups of kMGroup row tiles; inside a group the
-        // row tiles of one channel tile are adjacent (they share its weights)
+    // tiles of an expert: groups of kMGroup row tiles; inside a group the row
+    // tiles of one channel tile are adjacent (they share its weights)
+    const auto locate = [&](int64_t idx) {
+        const int64_t work = base + idx;
         TileAt at;
-        at.e = __builtin_amdgcn_readfirstlane(find_expert(tile_start, p.E, (int32_t)(work / n_tiles)));
-        const int32_t e_first = __builtin_amdgcn_readfirstlane(tile_start[at.e]);
-        const int32_t e_tiles = __builtin_amdgcn_readfirstlane(tile_start[at.e + 1]) - e_first;
+        at.e = scalar(find_expert(tile_start, p.E, (int32_t)(work / n_tiles)));
+        const int32_t e_first = scalar(tile_start[at.e]);
+        const int32_t e_tiles = scalar(tile_start[at.e + 1]) - e_first;
         const int64_t local = work - (int64_t)e_first * n_tiles;
         const int32_t grp = (int32_t)(local / ((int64_t)kMGroup * n_tiles));
         const int32_t in_grp = (int32_t)(local - (int64_t)grp * kMGroup * n_tiles);
         const int32_t grp_rows = min(kMGroup, e_tiles - grp * kMGroup);
-        at.nt = __builtin_amdgcn_readfirstlane(in_grp / grp_rows);
-        const int32_t first = __builtin_amdgcn_readfirstlane((grp * kMGroup + in_grp % grp_rows) * BM);
+        at.nt = scalar(in_grp / grp_rows);
+        const int32_t first = scalar((grp * kMGroup + in_grp % grp_rows) * BM);
         const int32_t count =
-            __builtin_amdgcn_readfirstlane(p.recv_count != nullptr ? p.recv_count[at.e] : p.dense_rows);
-        const int32_t seg = __builtin_amdgcn_readfirstlane(p.recv_count != nullptr ? p.expert_offset[at.e] : 0);
+            scalar(p.recv_count != nullptr ? p.recv_count[at.e] : p.dense_rows);
+        const int32_t seg = scalar(p.recv_count != nullptr ? p.expert_offset[at.e] : 0);
         at.valid = min(BM, count - first);
         at.row0 = (int64_t)seg + first;
-        // a segment's last tile takes the code for its size
-        if (MT <= 2 || at.valid > BM / 2)
-            run_tile<QUANT, BM, SWIGLU, MT>(p, at, lds, wave_max);
-        else if (MT <= 4 || at.valid > BM / 4)
-            run_tile<QUANT, BM, SWIGLU, (MT > 2 ? MT / 2 : MT)>(p, at, lds, wave_max);
+        return at;
+    };
+    int64_t idx = blockIdx.x >> 3;
+    if (idx >= end)
+        return;
+    TileAt next = locate(idx);
+    start_tile<QUANT, SWIGLU, BM, NS>(p, next, st0, st1, wave, lane);
+    for (;;) {
+        const TileAt at = next.scalars();
+        idx += gridDim.x >> 3;
+        const bool more = idx < end;
+        if (more)
+            next = locate(idx);
+        // a tile that is not full takes the code for its size
+        constexpr int MT = BM / 16 / kWaveRows, M2 = (MT + 1) / 2, M1 = (MT + 3) / 4;
+        if (at.valid > M2 * 32)
+            run_tile<QUANT, SWIGLU, BM, NS, MT>(p, at, next, more, st0, st1, st2, wave, lane);
+        else if (at.valid > M1 * 32)
+            run_tile<QUANT, SWIGLU, BM, NS, M2>(p, at, next, more, st0, st1, st2, wave, lane);
         else
-            run_tile<QUANT, BM, SWIGLU, (MT > 4 ? MT / 4 : MT)>(p, at, lds, wave_max);
-        __syncthreads();  // LDS is reused by the next tile
+            run_tile<QUANT, SWIGLU, BM, NS, M1>(p, at, next, more, st0, st1, st2, wave, lane);
+        if (!more)
+            break;
     }
 }
 
@@ -513,16 +629,16 @@ hipError_t launch(const ExpertGemmArgs &p, hipStream_t stream)
     return hipGetLastError();
 }
 
-template <int QUANT, bool SWIGLU, int MT, int OCC>
+template <int QUANT, bool SWIGLU, int BM, int NS>
 hipError_t launch_tiles(const ExpertGemmArgs &p, hipStream_t stream)
 {
-    constexpr int BM = MT * 16;
     const int32_t n_tiles = SWIGLU ? p.n / 256 : (p.n + kTileN - 1) / kTileN;
     const int64_t parts = p.max_rows < p.E ? p.max_rows : p.E;
-    int64_t grid = ((p.max_rows / BM + parts) * n_tiles + 7) / 8 * 8;
-    const int64_t cap = (int64_t)1 << 30;
-    grid = grid < 8 ? 8 : grid > cap ? cap : grid;
-    hipLaunchKernelGGL((expert_gemm_tiles<QUANT, SWIGLU, MT, OCC>), dim3((uint32_t)grid), dim3(kGemmThreads), 0,
+    const int64_t tiles = (p.max_rows / BM + parts) * n_tiles;
+    // one block per compute unit (its stages fill LDS), a multiple of the 8 XCDs
+    const int64_t cus = (device_cu_count() + 7) / 8 * 8;
+    const int64_t grid = tiles < cus ? (tiles + 7) / 8 * 8 : cus;
+    hipLaunchKernelGGL((expert_gemm_tiles<QUANT, SWIGLU, BM, NS>), dim3((uint32_t)grid), dim3(kTileThreads), 0,
                        stream, p, n_tiles);
     return hipGetLastError();
 }
@@ -533,9 +649,11 @@ hipError_t launch_rows(const ExpertGemmArgs &p, hipStream_t stream)
     const int64_t per_expert = p.max_rows / p.E;
     if (per_expert <= 16)
         return launch<QUANT, 1, SWIGLU>(p, stream);
-    if (per_expert <= 128)
-        return launch_tiles<QUANT, SWIGLU, 4, 2>(p, stream);
-    return launch_tiles<QUANT, SWIGLU, 8, 2>(p, stream);
+    const int64_t parts = p.max_rows < p.E ? p.max_rows : p.E;
+    const int64_t tiles = (p.max_rows / 256 + parts) * ((p.n + kTileN - 1) / kTileN);
+    if (per_expert <= 512 || tiles < device_cu_count())
+        return launch_tiles<QUANT, SWIGLU, 128, 3>(p, stream);
+    return launch_tiles<QUANT, SWIGLU, 256, 2>(p, stream);
 }
 
 template <bool SWIGLU>
