@@ -80,10 +80,17 @@ moe_status_t check_layer(const moe_config_t *cfg, int32_t inter)
     return MOE_OK;
 }
 
+// Workspace of a call: the experts' token masks (room for every pair, in whole
+// 16 bytes), then h.
+size_t layer_mask_bytes(const moe_config_t &c, int32_t tokens)
+{
+    return ((size_t)tokens * c.num_topk * sizeof(uint64_t) + 15) / 16 * 16;
+}
+
 size_t layer_bytes(const moe_config_t &c, int32_t tokens, int32_t inter)
 {
-    const size_t t = tokens < MOE_LAYER_MAX_TOKENS ? tokens : MOE_LAYER_MAX_TOKENS;
-    return t * c.num_topk * inter * sizeof(uint16_t);
+    const int32_t t = tokens < MOE_LAYER_MAX_TOKENS ? tokens : MOE_LAYER_MAX_TOKENS;
+    return layer_mask_bytes(c, t) + (size_t)t * c.num_topk * inter * sizeof(uint16_t);
 }
 
 }  // namespace
@@ -196,7 +203,8 @@ moe_status_t moe_layer_fused(const moe_config_t *cfg, int32_t num_tokens, int32_
     a.w13_scale = w13_scale;
     a.w2 = static_cast<const uint8_t *>(w2);
     a.w2_scale = w2_scale;
-    a.h = static_cast<uint16_t *>(workspace);
+    a.masks = static_cast<uint64_t *>(workspace);
+    a.h = reinterpret_cast<uint16_t *>(static_cast<char *>(workspace) + layer_mask_bytes(*cfg, num_tokens));
     a.out = out;
     a.T = num_tokens;
     a.K = cfg->num_topk;

@@ -56,6 +56,7 @@ struct LayerArgs {
     const void *w13_scale;
     const uint8_t *w2;
     const void *w2_scale;
+    uint64_t *masks;               // workspace: tokens of each expert slot [min(T * K, E)]
     uint16_t *h;                   // workspace: bf16 [T * K, inter]
     uint16_t *out;
     int32_t T, K, E, H, I;
