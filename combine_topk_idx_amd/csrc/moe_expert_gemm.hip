@@ -85,6 +85,12 @@ struct TileAt {
     }
 };
 
+// Two 16-byte pieces as one operand.
+__device__ __forceinline__ dev::i32x8 join(const dev::u32x4 &l, const dev::u32x4 &h)
+{
+    return dev::i32x8{(int)l[0], (int)l[1], (int)l[2], (int)l[3], (int)h[0], (int)h[1], (int)h[2], (int)h[3]};
+}
+
 // Writes a wave's results: rows 16 MT wr + 16 i + (lane % 16), channels n0[f] + 4
 // (lane / 16) + j.  bf16 outputs, or (SWIGLU; fragments f < 2 hold the gate,
 // f >= 2 the up products) SwiGLU and quantization, block-wide: the WC waves of
@@ -165,100 +171,132 @@ __device__ __forceinline__ void write_tile(const ExpertGemmArgs &p, dev::f32x4 (
     }
 }
 
-template <int QUANT, int MT, bool SWIGLU>
-__global__ __launch_bounds__(kGemmThreads) void expert_gemm_kernel(ExpertGemmArgs p, int32_t n_tiles)
+// ---------------------------------------------------------------------------
+// Few rows per expert: 16 rows x 256 channels per block of 4 waves.
+//
+// Bound by the weights' bytes: a wave streams its own 64 channels straight to
+// registers, the next block's loads in flight while one is multiplied, with no
+// barrier in the loop; the rows come from L2.  SwiGLU goes through bf16
+// operands (see multiply_stage), whose conversions are free here.
+// ---------------------------------------------------------------------------
+
+template <int QUANT, bool SWIGLU>
+__global__ __launch_bounds__(kGemmThreads) void expert_gemm_stream(ExpertGemmArgs p, int32_t n_tiles)
 {
-    constexpr int BM = MT * 16;
+    constexpr int BM = 16;
     __shared__ int32_t tile_start[kMaxExperts + 1];
     __shared__ int32_t red[kGemmWaves];
     __shared__ float wave_max[kGemmWaves][BM];
-    const int tid = threadIdx.x;
-    const int lane = tid & (kWave - 1);
-    const int wave = __builtin_amdgcn_readfirstlane(tid / kWave);
+    const int lane = threadIdx.x & (kWave - 1);
+    const int wave = scalar(threadIdx.x / kWave);
     const int r = lane & 15, g = lane >> 4;
     const int KB = p.k / kQuantGroup;
     const int KW = (KB + 3) / 4;
+    const int NBn = (p.n + kQuantGroup - 1) / kQuantGroup;
     scan_tiles<BM, kGemmThreads>(p.recv_count, p.E, p.dense_rows, tile_start, red);
-    const int64_t n_work = (int64_t)tile_start[p.E] * n_tiles;
+    const int64_t n_work = (int64_t)scalar(tile_start[p.E]) * n_tiles;
 
     for (int64_t work = blockIdx.x; work < n_work; work += gridDim.x) {
         const int32_t m = (int32_t)(work / n_tiles);
-        const int32_t nt = (int32_t)(work - (int64_t)m * n_tiles);
-        const int e = __builtin_amdgcn_readfirstlane(find_expert(tile_start, p.E, m));
-        const int32_t first = (m - tile_start[e]) * BM;
-        const int64_t seg = p.recv_count != nullptr ? p.expert_offset[e] : 0;
-        const int32_t count = p.recv_count != nullptr ? p.recv_count[e] : p.dense_rows;
-        const int32_t valid = min(BM, count - first);
-        const int64_t row0 = seg + first;
+        TileAt at;
+        at.nt = scalar((int32_t)(work - (int64_t)m * n_tiles));
+        at.e = scalar(find_expert(tile_start, p.E, m));
+        const int32_t first = scalar((m - tile_start[at.e]) * BM);
+        const int32_t count = scalar(p.recv_count != nullptr ? p.recv_count[at.e] : p.dense_rows);
+        at.valid = min(BM, count - first);
+        at.row0 = (int64_t)scalar(p.recv_count != nullptr ? p.expert_offset[at.e] : 0) + first;
 
-        // this lane's row of each row group, and this wave's channel fragments
-        int64_t arow[MT];
-#pragma unroll
-        for (int i = 0; i < MT; ++i)
-            arow[i] = row0 + min(i * 16 + r, valid - 1);
-        int32_t n0[kNF];
-        int64_t wrow[kNF];
+        const int64_t arow = at.row0 + min(r, at.valid - 1);
+        int64_t wrow[kNF], nb[kNF];
 #pragma unroll
         for (int f = 0; f < kNF; ++f) {
-            if constexpr (SWIGLU)
-                n0[f] = nt * 128 + wave * 32 + (f & 1) * 16 + (f >= 2 ? p.n / 2 : 0);
-            else
-                n0[f] = nt * kTileN + wave * 64 + f * 16;
-            wrow[f] = (int64_t)e * p.n + min(n0[f] + r, p.n - 1);
+            const int32_t c = SWIGLU ? at.nt * 128 + wave * 32 + (f & 1) * 16 + (f >= 2 ? p.n / 2 : 0)
+                                     : at.nt * kTileN + wave * 64 + f * 16;
+            wrow[f] = (int64_t)at.e * p.n + min(c + r, p.n - 1);
+            nb[f] = (int64_t)at.e * NBn + min(c, p.n - 1) / kQuantGroup;
         }
-        dev::f32x4 acc[kNF][MT];
+        dev::f32x4 acc[kNF][1];
 #pragma unroll
         for (int f = 0; f < kNF; ++f)
-#pragma unroll
-            for (int i = 0; i < MT; ++i)
-                acc[f][i] = dev::f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+            acc[f][0] = dev::f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 
-        const int NBn = (p.n + kQuantGroup - 1) / kQuantGroup;
-        for (int kb = 0; kb < KB; ++kb) {
-            dev::i32x8 wf[kNF];
-            float swf[kNF];
-            int swb[kNF];
+        struct Stage {
+            dev::u32x4 w[kNF][2], x[2];
+            uint32_t sw[kNF], sx;  // scales as they are stored
+        };
+        const auto fill = [&](Stage &st, int kb) {
+            const int64_t at_k = (int64_t)kb * kQuantGroup + 16 * g;
 #pragma unroll
             for (int f = 0; f < kNF; ++f) {
-                wf[f] = dev::load_frag(p.w + wrow[f] * p.k + (int64_t)kb * kQuantGroup, g);
-                const int64_t nb = (int64_t)e * NBn + min(n0[f], p.n - 1) / kQuantGroup;
-                if constexpr (QUANT == MOE_QUANT_FP8_F32)
-                    swf[f] = static_cast<const float *>(p.w_scale)[nb * KB + kb];
-                else if constexpr (QUANT == MOE_QUANT_FP8_UE8M0)
-                    swb[f] = static_cast<const uint8_t *>(p.w_scale)[nb * KW * 4 + kb];
+                const uint8_t *src = p.w + wrow[f] * p.k + at_k;
+                st.w[f][0] = *reinterpret_cast<const dev::u32x4 *>(src);
+                st.w[f][1] = *reinterpret_cast<const dev::u32x4 *>(src + 64);
+                if constexpr (QUANT == MOE_QUANT_FP8_UE8M0)
+                    st.sw[f] = static_cast<const uint8_t *>(p.w_scale)[nb[f] * KW * 4 + kb];
                 else
-                    swb[f] = static_cast<const uint8_t *>(p.w_scale)[wrow[f] * KB * 4 + kb * 4 + g];
+                    st.sw[f] = static_cast<const uint32_t *>(
+                        p.w_scale)[(QUANT == MOE_QUANT_FP8_F32 ? nb[f] : wrow[f]) * KB + kb];
             }
+            const uint8_t *src = p.a + arow * p.k + at_k;
+            st.x[0] = *reinterpret_cast<const dev::u32x4 *>(src);
+            st.x[1] = *reinterpret_cast<const dev::u32x4 *>(src + 64);
+            if constexpr (QUANT == MOE_QUANT_FP8_UE8M0)
+                st.sx = static_cast<const uint8_t *>(p.a_scale)[arow * KW * 4 + kb];
+            else
+                st.sx = static_cast<const uint32_t *>(p.a_scale)[arow * KB + kb];
+            __builtin_amdgcn_sched_barrier(0);
+        };
+        const auto use = [&](const Stage &st) {
+            const dev::f32x4 z = {0.0f, 0.0f, 0.0f, 0.0f};
+            dev::bf16x8 xv[4];
+            if constexpr (SWIGLU)
+                dev::block_to_bf16<QUANT>(st.x[0], st.x[1], st.sx, g, xv);
 #pragma unroll
-            for (int i = 0; i < MT; ++i) {
-                const dev::i32x8 af = dev::load_frag(p.a + arow[i] * p.k + (int64_t)kb * kQuantGroup, g);
-                float saf = 0.0f;
-                int sab = 0;
-                if constexpr (QUANT == MOE_QUANT_FP8_F32)
-                    saf = static_cast<const float *>(p.a_scale)[arow[i] * KB + kb];
-                else if constexpr (QUANT == MOE_QUANT_FP8_UE8M0)
-                    sab = static_cast<const uint8_t *>(p.a_scale)[arow[i] * KW * 4 + kb];
-                else
-                    sab = static_cast<const uint8_t *>(p.a_scale)[arow[i] * KB * 4 + kb * 4 + g];
+            for (int f = 0; f < kNF; ++f) {
+                dev::f32x4 d = QUANT == MOE_QUANT_FP8_F32 ? z : acc[f][0];
+                if constexpr (SWIGLU) {
+                    dev::bf16x8 wv[4];
+                    dev::block_to_bf16<QUANT>(st.w[f][0], st.w[f][1], st.sw[f], g, wv);
 #pragma unroll
-                for (int f = 0; f < kNF; ++f) {
-                    if constexpr (QUANT == MOE_QUANT_FP8_F32) {
-                        const dev::f32x4 z = {0.0f, 0.0f, 0.0f, 0.0f};
-                        const dev::f32x4 d =
-                            __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(wf[f], af, z, 0, 0, 0, 0, 0, 0);
-                        const float s = saf * swf[f];
+                    for (int j = 0; j < 4; ++j)
+                        d = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wv[j], xv[j], d, 0, 0, 0);
+                } else if constexpr (QUANT == MOE_QUANT_FP8_F32) {
+                    d = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
+                        join(st.w[f][0], st.w[f][1]), join(st.x[0], st.x[1]), d, 0, 0, 0, 0, 0, 0);
+                } else {
+                    const int shift = QUANT == MOE_QUANT_MXFP8 ? 8 * g : 0;
+                    d = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
+                        join(st.w[f][0], st.w[f][1]), join(st.x[0], st.x[1]), d, 0, 0, 0, (int)(st.sw[f] >> shift), 0,
+                        (int)(st.sx >> shift));
+                }
+                if constexpr (QUANT == MOE_QUANT_FP8_F32) {
+                    const float s = __uint_as_float(st.sx) * __uint_as_float(st.sw[f]);
 #pragma unroll
-                        for (int j = 0; j < 4; ++j)
-                            acc[f][i][j] = __builtin_fmaf(d[j], s, acc[f][i][j]);
-                    } else {
-                        acc[f][i] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(wf[f], af, acc[f][i], 0, 0, 0,
-                                                                                      swb[f], 0, sab);
-                    }
+                    for (int j = 0; j < 4; ++j)
+                        acc[f][0][j] = __builtin_fmaf(d[j], s, acc[f][0][j]);
+                } else {
+                    acc[f][0] = d;
                 }
             }
+            __builtin_amdgcn_sched_barrier(0);
+        };
+        Stage s0, s1;
+        int kb = 0;
+        fill(s0, 0);
+        for (; kb + 2 < KB; kb += 2) {
+            fill(s1, kb + 1);
+            use(s0);
+            fill(s0, kb + 2);
+            use(s1);
         }
-
-        write_tile<QUANT, MT, SWIGLU, BM>(p, acc, TileAt{e, nt, valid, row0}, 0, wave, lane, wave_max);
+        if (kb + 1 < KB) {
+            fill(s1, kb + 1);
+            use(s0);
+            use(s1);
+        } else {
+            use(s0);
+        }
+        write_tile<QUANT, 1, SWIGLU, BM>(p, acc, at, 0, wave, lane, wave_max);
         __syncthreads();  // wave_max is rewritten by the next tile
     }
 }
@@ -290,9 +328,11 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer(const void *p, uint32_t
     return __builtin_amdgcn_make_buffer_rsrc((void *)(hi << 32 | lo), 0, scalar((int32_t)bytes),
                                              0x00020000);
 }
-__device__ __forceinline__ dev::i32x8 join(const dev::u32x4 &l, const dev::u32x4 &h)
+
+// Four of an operand's eight registers.
+__device__ __forceinline__ dev::u32x4 half(const dev::i32x8 &v, int at)
 {
-    return dev::i32x8{(int)l[0], (int)l[1], (int)l[2], (int)l[3], (int)h[0], (int)h[1], (int)h[2], (int)h[3]};
+    return dev::u32x4{(uint32_t)v[at], (uint32_t)v[at + 1], (uint32_t)v[at + 2], (uint32_t)v[at + 3]};
 }
 
 // Memory -> LDS: BYTES per lane, lane l to dst + l * BYTES.
@@ -421,7 +461,12 @@ struct TileLoads {
 // fragments, while block `kb_load` loads into the stage `free`: its loads are
 // spread over the matrix instructions (all at once they would hold up the
 // wave's LDS reads until the address unit has taken them).
-template <int QUANT, bool SWIGLU, int BM, int MT>
+//
+// EXACT: through bf16 operands.  The 8-bit instruction adds its products eight
+// at a time, aligned to the largest of the eight, and drops what lies 13 binary
+// places below that one: 1.4e-5 (rms) of a block's result, where the bf16 one
+// stays near 1e-8 at half the rate.
+template <int QUANT, bool SWIGLU, int BM, int MT, bool EXACT>
 __device__ __forceinline__ void multiply_stage(dev::f32x4 (&acc)[kNF][MT], const uint8_t *st, int wr, int wc, int lane,
                                                int u, const TileLoads<QUANT, SWIGLU, BM> &loads, uint8_t *free,
                                                int kb_load)
@@ -467,10 +512,22 @@ __device__ __forceinline__ void multiply_stage(dev::f32x4 (&acc)[kNF][MT], const
             const float s0 = __uint_as_float(sx[i & 1]) * swf[0];
             const float s1 = SWIGLU ? __uint_as_float(sx[i & 1]) * swf[1] : s0;
             dev::f32x4 d[kNF];
+            dev::bf16x8 xv[4];
+            if constexpr (EXACT)
+                dev::block_to_bf16<QUANT>(half(x[i & 1], 0), half(x[i & 1], 4), 0, g, xv);
 #pragma unroll
             for (int f = 0; f < kNF; ++f) {
                 const dev::f32x4 z = {0.0f, 0.0f, 0.0f, 0.0f};
-                d[f] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(w[f], x[i & 1], z, 0, 0, 0, 0, 0, 0);
+                if constexpr (EXACT) {
+                    dev::bf16x8 wv[4];
+                    dev::block_to_bf16<QUANT>(half(w[f], 0), half(w[f], 4), 0, g, wv);
+                    d[f] = z;
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        d[f] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wv[j], xv[j], d[f], 0, 0, 0);
+                } else {
+                    d[f] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(w[f], x[i & 1], z, 0, 0, 0, 0, 0, 0);
+                }
             }
             loads.template issue<i * kLoads / MT, (i + 1) * kLoads / MT>(free, kb_load);
 #pragma unroll
@@ -520,28 +577,37 @@ __device__ __forceinline__ void run_tile(const ExpertGemmArgs &p, const TileAt &
 #pragma unroll
         for (int i = 0; i < MT; ++i)
             acc[f][i] = dev::f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-    const auto step = [&](uint8_t *cur, uint8_t *free, int kb) {
+    const auto step = [&](auto exact, uint8_t *cur, uint8_t *free, int kb) {
         wait_and_meet<kAhead>();
-        multiply_stage<QUANT, SWIGLU, BM, MT>(acc, cur, wr, wc, lane, loads.block(kb) & 3, loads, free, kb + NS - 1);
+        multiply_stage<QUANT, SWIGLU, BM, MT, decltype(exact)::value>(acc, cur, wr, wc, lane, loads.block(kb) & 3, loads, free, kb + NS - 1);
     };
+    // The fp32 scales of SwiGLU's output would show the 8-bit instruction's error
+    // (1.15e-5 rms of them): every third block goes through bf16 operands, which
+    // leaves 9.3e-6 and costs 20% (gate and up products of 32,768 skewed rows, 64
+    // experts, 7168 -> 2 x 2048: 1.31 -> 1.56 ms; all blocks: 2e-7, 2.06 ms).
+    // Outputs in bf16 or with power-of-two scales do not show it.
+    constexpr bool kMixed = QUANT == MOE_QUANT_FP8_F32 && SWIGLU;
+    static_assert(!kMixed || NS == 3, "one block of three");
+    const std::false_type fast;
+    const std::bool_constant<kMixed> mixed;
     int kb = 0;
     if constexpr (NS == 3) {
         for (; kb + 3 <= KB; kb += 3) {
-            step(st0, st2, kb);
-            step(st1, st0, kb + 1);
-            step(st2, st1, kb + 2);
+            step(mixed, st0, st2, kb);
+            step(fast, st1, st0, kb + 1);
+            step(fast, st2, st1, kb + 2);
         }
         if (kb < KB)
-            step(st0, st2, kb);
+            step(mixed, st0, st2, kb);
         if (kb + 1 < KB)
-            step(st1, st0, kb + 1);
+            step(fast, st1, st0, kb + 1);
     } else {
         for (; kb + 2 <= KB; kb += 2) {
-            step(st0, st1, kb);
-            step(st1, st0, kb + 1);
+            step(fast, st0, st1, kb);
+            step(fast, st1, st0, kb + 1);
         }
         if (kb < KB)
-            step(st0, st1, kb);
+            step(fast, st0, st1, kb);
     }
     wait_and_meet<0>();
     if (more)
@@ -614,18 +680,17 @@ __global__ __launch_bounds__(kTileThreads) void expert_gemm_tiles(ExpertGemmArgs
     }
 }
 
-template <int QUANT, int MT, bool SWIGLU>
-hipError_t launch(const ExpertGemmArgs &p, hipStream_t stream)
+template <int QUANT, bool SWIGLU>
+hipError_t launch_stream(const ExpertGemmArgs &p, hipStream_t stream)
 {
-    constexpr int BM = MT * 16;
     const int32_t n_tiles = SWIGLU ? p.n / 256 : (p.n + kTileN - 1) / kTileN;
     // a segment's last tile is partial: at most one more tile per expert that has rows
     const int64_t parts = p.max_rows < p.E ? p.max_rows : p.E;
-    int64_t grid = (p.max_rows / BM + parts) * n_tiles;
+    const int64_t tiles = (p.max_rows / 16 + parts) * n_tiles;
     const int64_t cap = (int64_t)1 << 30;
-    grid = grid < 1 ? 1 : grid > cap ? cap : grid;
-    hipLaunchKernelGGL((expert_gemm_kernel<QUANT, MT, SWIGLU>), dim3((uint32_t)grid), dim3(kGemmThreads), 0, stream,
-                       p, n_tiles);
+    const int64_t grid = tiles < 1 ? 1 : tiles > cap ? cap : tiles;
+    hipLaunchKernelGGL((expert_gemm_stream<QUANT, SWIGLU>), dim3((uint32_t)grid), dim3(kGemmThreads), 0, stream, p,
+                       n_tiles);
     return hipGetLastError();
 }
 
@@ -648,12 +713,14 @@ hipError_t launch_rows(const ExpertGemmArgs &p, hipStream_t stream)
 {
     const int64_t per_expert = p.max_rows / p.E;
     if (per_expert <= 16)
-        return launch<QUANT, 1, SWIGLU>(p, stream);
-    const int64_t parts = p.max_rows < p.E ? p.max_rows : p.E;
-    const int64_t tiles = (p.max_rows / 256 + parts) * ((p.n + kTileN - 1) / kTileN);
-    if (per_expert <= 512 || tiles < device_cu_count())
-        return launch_tiles<QUANT, SWIGLU, 128, 3>(p, stream);
-    return launch_tiles<QUANT, SWIGLU, 256, 2>(p, stream);
+        return launch_stream<QUANT, SWIGLU>(p, stream);
+    if constexpr (QUANT != MOE_QUANT_FP8_F32 || !SWIGLU) {
+        const int64_t parts = p.max_rows < p.E ? p.max_rows : p.E;
+        const int64_t tiles = (p.max_rows / 256 + parts) * ((p.n + kTileN - 1) / kTileN);
+        if (per_expert > 512 && tiles >= device_cu_count())
+            return launch_tiles<QUANT, SWIGLU, 256, 2>(p, stream);
+    }
+    return launch_tiles<QUANT, SWIGLU, 128, 3>(p, stream);
 }
 
 template <bool SWIGLU>

@@ -24,20 +24,6 @@ constexpr int kDownWaves = 8;                         // down: waves that share 
 constexpr int kRing1 = 3, kRing2 = 2;
 constexpr int kLayerMaxPairs = MOE_LAYER_MAX_TOKENS * kMaxTopk;
 
-// 16 E4M3 values (16 bytes) times a power of two -> two bf16 operands of 8.
-__device__ __forceinline__ void to_bf16(const dev::u32x4 &v, float scale, dev::bf16x8 &lo, dev::bf16x8 &hi)
-{
-#pragma unroll
-    for (int j = 0; j < 2; ++j) {
-        const dev::bf16x2 a = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(v[j], scale, false);
-        const dev::bf16x2 b = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(v[j], scale, true);
-        lo[4 * j] = a[0], lo[4 * j + 1] = a[1], lo[4 * j + 2] = b[0], lo[4 * j + 3] = b[1];
-        const dev::bf16x2 c = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(v[2 + j], scale, false);
-        const dev::bf16x2 d = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(v[2 + j], scale, true);
-        hi[4 * j] = c[0], hi[4 * j + 1] = c[1], hi[4 * j + 2] = d[0], hi[4 * j + 3] = d[1];
-    }
-}
-
 // One lane's part of a 16-row weight strip (row `row` of [rows, k], or a clamped
 // one): the 128 channels of block kb as four bf16 operands of 8 channels each
 // (channels 16 g .. of each 64: the columns use the same order), multiplied by
@@ -95,16 +81,8 @@ struct Weights {
 #pragma unroll
             for (int j = 0; j < 4; ++j)
                 wv[j] = __builtin_bit_cast(dev::bf16x8, v[j]);
-        } else if constexpr (QUANT == MOE_QUANT_FP8_F32) {
-            to_bf16(v[0], 1.0f, wv[0], wv[1]);
-            to_bf16(v[1], 1.0f, wv[2], wv[3]);
-        } else if constexpr (QUANT == MOE_QUANT_FP8_UE8M0) {
-            to_bf16(v[0], __uint_as_float(s << 23), wv[0], wv[1]);
-            to_bf16(v[1], __uint_as_float(s << 23), wv[2], wv[3]);
-        } else {  // this lane's 16 channels lie in MX blocks g / 2 and 2 + g / 2
-            const uint32_t two = s >> (4 * (g & 2));
-            to_bf16(v[0], __uint_as_float((two & 0xFFu) << 23), wv[0], wv[1]);
-            to_bf16(v[1], __uint_as_float((two >> 16 & 0xFFu) << 23), wv[2], wv[3]);
+        } else {
+            dev::block_to_bf16<QUANT>(v[0], v[1], s, g, wv);
         }
     }
 };

@@ -34,6 +34,39 @@ __device__ __forceinline__ uint32_t bf16_bits(float f)
 }
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) { return bf16_bits(lo) | bf16_bits(hi) << 16; }
 
+// 16 E4M3 values (16 bytes) times a power of two -> two bf16 operands of 8, exact.
+__device__ __forceinline__ void to_bf16(const u32x4 &v, float scale, bf16x8 &lo, bf16x8 &hi)
+{
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+        const bf16x2 a = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(v[j], scale, false);
+        const bf16x2 b = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(v[j], scale, true);
+        lo[4 * j] = a[0], lo[4 * j + 1] = a[1], lo[4 * j + 2] = b[0], lo[4 * j + 3] = b[1];
+        const bf16x2 c = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(v[2 + j], scale, false);
+        const bf16x2 d = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(v[2 + j], scale, true);
+        hi[4 * j] = c[0], hi[4 * j + 1] = c[1], hi[4 * j + 2] = d[0], hi[4 * j + 3] = d[1];
+    }
+}
+
+// One lane's share of a row's block of 128 channels -- the 16 bytes at 16 g (lo)
+// and at 64 + 16 g (hi) -- as four bf16 operands of v_mfma_f32_16x16x32_bf16,
+// times the block's scale where that is a power of two (`s`: as it is stored; the
+// word of four bytes for MXFP8, whose blocks g / 2 and 2 + g / 2 the lane has).
+template <int QUANT>
+__device__ __forceinline__ void block_to_bf16(const u32x4 &lo, const u32x4 &hi, uint32_t s, int g, bf16x8 v[4])
+{
+    float a = 1.0f, b = 1.0f;
+    if constexpr (QUANT == MOE_QUANT_FP8_UE8M0) {
+        a = b = __uint_as_float(s << 23);
+    } else if constexpr (QUANT == MOE_QUANT_MXFP8) {
+        const uint32_t two = s >> (4 * (g & 2));
+        a = __uint_as_float((two & 0xFFu) << 23);
+        b = __uint_as_float((two >> 16 & 0xFFu) << 23);
+    }
+    to_bf16(lo, a, v[0], v[1]);
+    to_bf16(hi, b, v[2], v[3]);
+}
+
 // silu(g) * u
 __device__ __forceinline__ float swiglu(float g, float u) { return g / (1.0f + expf(-g)) * u; }
 
