@@ -34,6 +34,13 @@ __device__ __forceinline__ int32_t scalar(int32_t v)
     return __builtin_amdgcn_readfirstlane(v);
 }
 
+// Word i (uniform) of an array that the kernel does not write, by a scalar load:
+// a vector load would wait for every load before it, whole stages of a tile.
+__device__ __forceinline__ int32_t word_of(const int32_t *a, int32_t i)
+{
+    return reinterpret_cast<const __attribute__((address_space(4))) int32_t *>((uint64_t)a)[i];
+}
+
 // tile_start[e] = row tiles of BM rows before expert e; [E] = all.  Block-wide,
 // ends with a barrier.
 template <int BM, int NT>
@@ -91,6 +98,29 @@ __device__ __forceinline__ dev::i32x8 join(const dev::u32x4 &l, const dev::u32x4
     return dev::i32x8{(int)l[0], (int)l[1], (int)l[2], (int)l[3], (int)h[0], (int)h[1], (int)h[2], (int)h[3]};
 }
 
+// Buffer descriptor over `bytes` bytes (loads past them return 0), the same in
+// every lane.
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer(const void *p, uint32_t bytes)
+{
+    const uint64_t a = (uint64_t)p;
+    const uint64_t lo = (uint32_t)scalar((int32_t)a);
+    const uint64_t hi = (uint32_t)scalar((int32_t)(a >> 32));
+    return __builtin_amdgcn_make_buffer_rsrc((void *)(hi << 32 | lo), 0, scalar((int32_t)bytes),
+                                             0x00020000);
+}
+
+// Store number `count - 1` and those before it without effect: past the end.
+template <int COUNT>
+__device__ __forceinline__ void store_nothing(__amdgpu_buffer_rsrc_t out)
+{
+#pragma unroll
+    for (int i = 0; i < COUNT; ++i)
+        __builtin_amdgcn_raw_buffer_store_b128(dev::u32x4{0, 0, 0, 0}, out, 0x80000000u, 0, 0);
+}
+
+// Stores of a wave for a tile of BM rows whose results are bf16 (write_tile).
+constexpr int kTileStores(int bm) { return bm <= 16 ? 2 : bm / 16; }
+
 // Writes a wave's results: rows 16 MT wr + 16 i + (lane % 16), channels n0[f] + 4
 // (lane / 16) + j.  bf16 outputs, or (SWIGLU; fragments f < 2 hold the gate,
 // f >= 2 the up products) SwiGLU and quantization, block-wide: the WC waves of
@@ -101,18 +131,29 @@ __device__ __forceinline__ void write_tile(const ExpertGemmArgs &p, dev::f32x4 (
 {
     const int r = lane & 15, g = lane >> 4;
     if constexpr (!SWIGLU) {
+        // Two fragments' results change places between odd and even rows of 16
+        // lanes: a lane then has 8 adjacent channels of its row, and a store covers
+        // 64 bytes of each of 16 rows.  Rows and channels past the end go past the
+        // buffer's: every wave issues the same number of stores.
+        const __amdgpu_buffer_rsrc_t out = buffer(p.y + at.row0 * p.n, (uint32_t)at.valid * (uint32_t)p.n * 2);
 #pragma unroll
         for (int i = 0; i < MT; ++i) {
             const int32_t row = (wr * MT + i) * 16 + r;
 #pragma unroll
-            for (int f = 0; f < kNF; ++f) {
-                const int32_t n = at.nt * kTileN + wc * 64 + f * 16 + g * 4;
-                if (row < at.valid && n < p.n)
-                    *reinterpret_cast<uint2 *>(p.y + (at.row0 + row) * p.n + n) =
-                        make_uint2(dev::pack_bf16(acc[f][i][0], acc[f][i][1]),
-                                   dev::pack_bf16(acc[f][i][2], acc[f][i][3]));
+            for (int f = 0; f < kNF; f += 2) {
+                const auto lo = __builtin_amdgcn_permlane16_swap(dev::pack_bf16(acc[f][i][0], acc[f][i][1]),
+                                                                 dev::pack_bf16(acc[f + 1][i][0], acc[f + 1][i][1]),
+                                                                 false, false);
+                const auto hi = __builtin_amdgcn_permlane16_swap(dev::pack_bf16(acc[f][i][2], acc[f][i][3]),
+                                                                 dev::pack_bf16(acc[f + 1][i][2], acc[f + 1][i][3]),
+                                                                 false, false);
+                const int32_t n = at.nt * kTileN + wc * 64 + (f + (g & 1)) * 16 + (g >> 1) * 8;
+                const uint32_t off = row < at.valid && n < p.n ? ((uint32_t)row * (uint32_t)p.n + n) * 2 : 0x80000000u;
+                const dev::u32x4 v = {lo[0], hi[0], lo[1], hi[1]};
+                __builtin_amdgcn_raw_buffer_store_b128(v, out, off, 0, 0);
             }
         }
+        store_nothing<kTileStores(BM) - MT * 2>(out);
     } else {
         const int32_t inter = p.n / 2;
         // h in the place of the gate accumulators; largest magnitude per row and wave
@@ -202,9 +243,9 @@ __global__ __launch_bounds__(kGemmThreads) void expert_gemm_stream(ExpertGemmArg
         at.nt = scalar((int32_t)(work - (int64_t)m * n_tiles));
         at.e = scalar(find_expert(tile_start, p.E, m));
         const int32_t first = scalar((m - tile_start[at.e]) * BM);
-        const int32_t count = scalar(p.recv_count != nullptr ? p.recv_count[at.e] : p.dense_rows);
+        const int32_t count = p.recv_count != nullptr ? word_of(p.recv_count, at.e) : p.dense_rows;
         at.valid = min(BM, count - first);
-        at.row0 = (int64_t)scalar(p.recv_count != nullptr ? p.expert_offset[at.e] : 0) + first;
+        at.row0 = (int64_t)(p.recv_count != nullptr ? word_of(p.expert_offset, at.e) : 0) + first;
 
         const int64_t arow = at.row0 + min(r, at.valid - 1);
         int64_t wrow[kNF], nb[kNF];
@@ -318,17 +359,6 @@ constexpr int kTileWaves = kTileThreads / kWave;
 constexpr int kMGroup = 8;   // row tiles that walk the channel tiles together
 constexpr int kWaveRows = 2, kWaveCols = 4;  // waves over the tile's rows and channels
 
-// Buffer descriptor over `bytes` bytes (loads past them return 0), the same in
-// every lane.
-__device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer(const void *p, uint32_t bytes)
-{
-    const uint64_t a = (uint64_t)p;
-    const uint64_t lo = (uint32_t)scalar((int32_t)a);
-    const uint64_t hi = (uint32_t)scalar((int32_t)(a >> 32));
-    return __builtin_amdgcn_make_buffer_rsrc((void *)(hi << 32 | lo), 0, scalar((int32_t)bytes),
-                                             0x00020000);
-}
-
 // Four of an operand's eight registers.
 __device__ __forceinline__ dev::u32x4 half(const dev::i32x8 &v, int at)
 {
@@ -351,6 +381,7 @@ __device__ __forceinline__ void load_lds(__amdgpu_buffer_rsrc_t b, uint8_t *dst,
 template <int VM>
 __device__ __forceinline__ void wait_and_meet()
 {
+    static_assert(VM < 64, "the counter's range");
     asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(VM) : "memory");
 }
 
@@ -386,18 +417,13 @@ template <int QUANT, bool SWIGLU, int BM>
 struct TileLoads {
     __amdgpu_buffer_rsrc_t a, w[2], s;
     uint32_t ao[BM / 64], wo[SWIGLU ? 2 : 4], so;  // rows, weights (both halves alike with SWIGLU), scales
-    int KB, wave, rot;
-
-    // Tiles start their walk over the blocks at different ones: rows lie k bytes
-    // apart, so tiles in step would all read the same few channels of L2.
-    __device__ __forceinline__ int block(int kb) const { return kb + rot < KB ? kb + rot : kb + rot - KB; }
+    int KB, wave;
 
     __device__ __forceinline__ void set(const ExpertGemmArgs &p, const TileAt &at, int wave_, int lane)
     {
         wave = wave_;
         const uint32_t k = (uint32_t)p.k;
         KB = p.k / kQuantGroup;
-        rot = 0;
         const int SW = QUANT == MOE_QUANT_FP8_UE8M0 ? (KB + 3) / 4 : KB;  // scale words of a row
         const int NBn = (p.n + kQuantGroup - 1) / kQuantGroup;
         // 16-byte piece c of a row sits at position c ^ ((row >> 1) & 7) in LDS:
@@ -439,7 +465,7 @@ struct TileLoads {
     {
         constexpr int kA = BM / 64;
         const uint32_t past = kb < KB ? 0u : 0x80000000u;
-        const int b = kb < KB ? block(kb) : 0;
+        const int b = kb < KB ? kb : 0;
         const uint32_t at_k = (uint32_t)b * kQuantGroup;
 #pragma unroll
         for (int j = FROM; j < TO; ++j) {
@@ -577,9 +603,12 @@ __device__ __forceinline__ void run_tile(const ExpertGemmArgs &p, const TileAt &
 #pragma unroll
         for (int i = 0; i < MT; ++i)
             acc[f][i] = dev::f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-    const auto step = [&](auto exact, uint8_t *cur, uint8_t *free, int kb) {
-        wait_and_meet<kAhead>();
-        multiply_stage<QUANT, SWIGLU, BM, MT, decltype(exact)::value>(acc, cur, wr, wc, lane, loads.block(kb) & 3, loads, free, kb + NS - 1);
+    // FIRST: the stores of the tile before may still be on their way, behind the
+    // loads of this tile's first NS - 1 stages
+    const auto step = [&](auto first, auto exact, uint8_t *cur, uint8_t *free, int kb) {
+        wait_and_meet<kAhead + (decltype(first)::value && !SWIGLU ? kTileStores(BM) : 0)>();
+        multiply_stage<QUANT, SWIGLU, BM, MT, decltype(exact)::value>(acc, cur, wr, wc, lane, kb & 3, loads, free,
+                                                                      kb + NS - 1);
     };
     // The fp32 scales of SwiGLU's output would show the 8-bit instruction's error
     // (1.15e-5 rms of them): every third block goes through bf16 operands, which
@@ -588,26 +617,32 @@ __device__ __forceinline__ void run_tile(const ExpertGemmArgs &p, const TileAt &
     // Outputs in bf16 or with power-of-two scales do not show it.
     constexpr bool kMixed = QUANT == MOE_QUANT_FP8_F32 && SWIGLU;
     static_assert(!kMixed || NS == 3, "one block of three");
-    const std::false_type fast;
+    const std::true_type first;
+    const std::false_type fast, later;
     const std::bool_constant<kMixed> mixed;
-    int kb = 0;
+    step(first, mixed, st0, NS == 3 ? st2 : st1, 0);
     if constexpr (NS == 3) {
-        for (; kb + 3 <= KB; kb += 3) {
-            step(mixed, st0, st2, kb);
-            step(fast, st1, st0, kb + 1);
-            step(fast, st2, st1, kb + 2);
+        if (KB > 1) {
+            step(first, fast, st1, st0, 1);
+            int kb = 2;
+            for (; kb + 3 <= KB; kb += 3) {
+                step(later, fast, st2, st1, kb);
+                step(later, mixed, st0, st2, kb + 1);
+                step(later, fast, st1, st0, kb + 2);
+            }
+            if (kb < KB)
+                step(later, fast, st2, st1, kb);
+            if (kb + 1 < KB)
+                step(later, mixed, st0, st2, kb + 1);
         }
-        if (kb < KB)
-            step(mixed, st0, st2, kb);
-        if (kb + 1 < KB)
-            step(fast, st1, st0, kb + 1);
     } else {
+        int kb = 1;
         for (; kb + 2 <= KB; kb += 2) {
-            step(fast, st0, st1, kb);
-            step(fast, st1, st0, kb + 1);
+            step(later, fast, st1, st0, kb);
+            step(later, fast, st0, st1, kb + 1);
         }
         if (kb < KB)
-            step(fast, st0, st1, kb);
+            step(later, fast, st1, st0, kb);
     }
     wait_and_meet<0>();
     if (more)
@@ -649,9 +684,8 @@ __global__ __launch_bounds__(kTileThreads) void expert_gemm_tiles(ExpertGemmArgs
         const int32_t grp_rows = min(kMGroup, e_tiles - grp * kMGroup);
         at.nt = scalar(in_grp / grp_rows);
         const int32_t first = scalar((grp * kMGroup + in_grp % grp_rows) * BM);
-        const int32_t count =
-            scalar(p.recv_count != nullptr ? p.recv_count[at.e] : p.dense_rows);
-        const int32_t seg = scalar(p.recv_count != nullptr ? p.expert_offset[at.e] : 0);
+        const int32_t count = p.recv_count != nullptr ? word_of(p.recv_count, at.e) : p.dense_rows;
+        const int32_t seg = p.recv_count != nullptr ? word_of(p.expert_offset, at.e) : 0;
         at.valid = min(BM, count - first);
         at.row0 = (int64_t)seg + first;
         return at;
@@ -661,6 +695,8 @@ __global__ __launch_bounds__(kTileThreads) void expert_gemm_tiles(ExpertGemmArgs
         return;
     TileAt next = locate(idx);
     start_tile<QUANT, SWIGLU, BM, NS>(p, next, st0, st1, wave, lane);
+    if constexpr (!SWIGLU)  // as many as behind the loads of every later tile (see step)
+        store_nothing<kTileStores(BM)>(buffer(p.y, 0));
     for (;;) {
         const TileAt at = next.scalars();
         idx += gridDim.x >> 3;

@@ -39,7 +39,7 @@ moe_status_t prepare_gemm(const moe_config_t *cfg, int32_t num_tokens, int32_t n
     if (n < 8 || n % 8 != 0 || k < kQuantGroup || k % kQuantGroup != 0)
         return MOE_ERR_INVALID_ARG;
     // a tile's rows and an expert's weight scales are addressed with 32-bit offsets
-    if (k > kMaxGemmK || (int64_t)n * (k / 32) > INT32_MAX)
+    if (n > kMaxGemmN || k > kMaxGemmK || (int64_t)n * (k / 32) > INT32_MAX)
         return MOE_ERR_UNSUPPORTED;
     if (handle == nullptr && cfg->num_experts != 1)
         return MOE_ERR_INVALID_ARG;

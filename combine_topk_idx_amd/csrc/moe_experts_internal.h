@@ -29,7 +29,9 @@ hipError_t launch_rmsnorm(const NormArgs &a, int32_t quant, hipStream_t stream);
 
 // ---- grouped products -----------------------------------------------------------
 
-constexpr int32_t kMaxGemmK = 1 << 22;  // input channels of a product: 256 rows stay below 2 GiB
+// Channels of a product: the 256 rows of a tile, read or written, stay within
+// 2 GiB of 32-bit offsets.
+constexpr int32_t kMaxGemmK = 1 << 22, kMaxGemmN = 1 << 22;
 
 struct ExpertGemmArgs {
     const uint8_t *a;              // [rows, k] E4M3

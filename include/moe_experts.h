@@ -76,7 +76,7 @@ moe_status_t moe_rmsnorm(const moe_config_t *cfg, int32_t num_tokens, const uint
  * neither read nor written.
  *
  *   n          output channels, a multiple of 8.
- *   k          input channels, a multiple of 128, at most 2^22, and
+ *   k          input channels, a multiple of 128.  n and k are at most 2^22 and
  *              n * k / 32 < 2^31 (larger: MOE_ERR_UNSUPPORTED).
  *   a          E4M3 [rows, k] and a_scale its scales in moe_dispatch's layout of
  *              out_scale (k in the place of H): dispatched rows, or the rows of

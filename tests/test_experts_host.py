@@ -167,6 +167,12 @@ def test_swiglu_refusals(lib, cfg, T, kw, code):
                                       a["h_scale"], None) == code
 
 
+def test_output_channels_past_the_limit(lib):
+    """256 rows of more than 2^22 output channels pass the products' 32-bit offsets."""
+    assert _gemm(lib, _cfg(), 0, n=1 << 22, k=128) == M.MOE_OK
+    assert _gemm(lib, _cfg(), 1, n=(1 << 22) + 8, k=128) == M.MOE_ERR_UNSUPPORTED
+
+
 # ---- few-token layer ----------------------------------------------------------------
 
 LAYER_OK = dict(inter=256, topk_idx=FAKE, topk_w=FAKE, x=FAKE, w13=FAKE, w13_scale=FAKE, w2=FAKE, w2_scale=FAKE,
