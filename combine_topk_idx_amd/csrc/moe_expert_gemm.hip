@@ -41,36 +41,47 @@ __device__ __forceinline__ int32_t word_of(const int32_t *a, int32_t i)
     return reinterpret_cast<const __attribute__((address_space(4))) int32_t *>((uint64_t)a)[i];
 }
 
-// tile_start[e] = row tiles of BM rows before expert e; [E] = all.  Block-wide,
-// ends with a barrier.
-template <int BM, int NT>
-__device__ inline void scan_tiles(const int32_t *recv_count, int32_t E, int32_t dense_rows, int32_t *tile_start,
-                                  int32_t *red)
+// tile_start[i] = row tiles of BM rows before expert G i; [ceil(E / G)] = all.
+// Block-wide, ends with a barrier.
+template <int BM, int NT, int G>
+__device__ inline void scan_tiles(const ExpertGemmArgs &p, int32_t *tile_start, int32_t *red)
 {
     const int tid = threadIdx.x, lane = tid & (kWave - 1), wave = tid / kWave;
-    const int per = (E + NT - 1) / NT;
-    const int e0 = min(E, tid * per), e1 = min(E, e0 + per);
+    const int groups = (p.E + G - 1) / G;
+    const int per = (groups + NT - 1) / NT;
+    const int e0 = min(groups, tid * per) * G, e1 = min(groups, (tid + 1) * per) * G;
+    const auto tiles = [&](int e) {
+        return ((e >= p.E ? 0 : p.recv_count != nullptr ? p.recv_count[e] : p.dense_rows) + BM - 1) / BM;
+    };
     int32_t local = 0;
     for (int e = e0; e < e1; ++e)
-        local += ((recv_count != nullptr ? recv_count[e] : dense_rows) + BM - 1) / BM;
+        local += tiles(e);
     const int32_t incl = dev::wave_inclusive_sum(local);
     if (lane == kWave - 1)
         red[wave] = incl;
     __syncthreads();
     int32_t run = dev::sum_before<NT / kWave>(red, wave) + incl - local;
     for (int e = e0; e < e1; ++e) {
-        tile_start[e] = run;
-        run += ((recv_count != nullptr ? recv_count[e] : dense_rows) + BM - 1) / BM;
+        if (e % G == 0)
+            tile_start[e / G] = run;
+        run += tiles(e);
     }
     if (tid == NT - 1)
-        tile_start[E] = run;
+        tile_start[groups] = run;
     __syncthreads();
 }
 
-// Expert of row tile m: the last e with tile_start[e] <= m.
-__device__ __forceinline__ int find_expert(const int32_t *tile_start, int32_t E, int32_t m)
+// An expert's rows: `first` of them lie in tiles before, its tiles start at
+// number `start`.
+struct ExpertAt {
+    int32_t e, start, rows;
+};
+
+// The expert that row tile m (uniform, below the number of all) belongs to.
+template <int BM, int G>
+__device__ __forceinline__ ExpertAt find_expert(const ExpertGemmArgs &p, const int32_t *tile_start, int32_t m)
 {
-    int lo = 0, hi = E;
+    int lo = 0, hi = (p.E + G - 1) / G;
     while (hi - lo > 1) {
         const int mid = (lo + hi) >> 1;
         if (scalar(tile_start[mid]) <= m)
@@ -78,7 +89,20 @@ __device__ __forceinline__ int find_expert(const int32_t *tile_start, int32_t E,
         else
             hi = mid;
     }
-    return lo;
+    if (p.recv_count == nullptr)
+        return ExpertAt{0, 0, p.dense_rows};
+    int32_t rows[G];
+#pragma unroll
+    for (int i = 0; i < G; ++i)
+        rows[i] = word_of(p.recv_count, min(lo * G + i, p.E - 1));
+    ExpertAt at = {lo * G, scalar(tile_start[lo]), rows[0]};
+#pragma unroll
+    for (int i = 1; i < G; ++i) {
+        const int32_t after = at.start + (at.rows + BM - 1) / BM;
+        if (m >= after)
+            at = ExpertAt{lo * G + i, after, rows[i]};
+    }
+    return at;
 }
 
 // A tile of work: rows [row0, row0 + valid) of expert e, channel tile nt.
@@ -118,8 +142,15 @@ __device__ __forceinline__ void store_nothing(__amdgpu_buffer_rsrc_t out)
         __builtin_amdgcn_raw_buffer_store_b128(dev::u32x4{0, 0, 0, 0}, out, 0x80000000u, 0, 0);
 }
 
-// Stores of a wave for a tile of BM rows whose results are bf16 (write_tile).
-constexpr int kTileStores(int bm) { return bm <= 16 ? 2 : bm / 16; }
+// Waits for this wave's LDS accesses, then for the block's other waves, and
+// leaves memory accesses on their way.
+__device__ __forceinline__ void meet()
+{
+    asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+}
+
+// Stores that a wave always issues for MT row fragments (write_tile).
+constexpr int kStores(int mt) { return 2 * mt; }
 
 // Writes a wave's results: rows 16 MT wr + 16 i + (lane % 16), channels n0[f] + 4
 // (lane / 16) + j.  bf16 outputs, or (SWIGLU; fragments f < 2 hold the gate,
@@ -129,6 +160,7 @@ template <int QUANT, int MT, bool SWIGLU, int BM>
 __device__ __forceinline__ void write_tile(const ExpertGemmArgs &p, dev::f32x4 (&acc)[kNF][MT], const TileAt &at,
                                            int wr, int wc, int lane, float (*wave_max)[BM])
 {
+    constexpr int kMaxMT = BM <= 16 ? 1 : BM / 32;
     const int r = lane & 15, g = lane >> 4;
     if constexpr (!SWIGLU) {
         // Two fragments' results change places between odd and even rows of 16
@@ -153,62 +185,68 @@ __device__ __forceinline__ void write_tile(const ExpertGemmArgs &p, dev::f32x4 (
                 __builtin_amdgcn_raw_buffer_store_b128(v, out, off, 0, 0);
             }
         }
-        store_nothing<kTileStores(BM) - MT * 2>(out);
+        store_nothing<kStores(kMaxMT) - kStores(MT)>(out);
     } else {
         const int32_t inter = p.n / 2;
-        // h in the place of the gate accumulators; largest magnitude per row and wave
+        const __amdgpu_buffer_rsrc_t out = buffer(p.h + at.row0 * inter, (uint32_t)at.valid * (uint32_t)inter);
+        constexpr int kScale = QUANT == MOE_QUANT_FP8_UE8M0 ? 1 : 4;  // bytes of 128 channels' scales
+        const int HB = inter / kQuantGroup, HW = (HB * kScale + 3) / 4 * 4;
+        const __amdgpu_buffer_rsrc_t scales =
+            buffer(static_cast<uint8_t *>(p.h_scale) + at.row0 * HW, (uint32_t)at.valid * (uint32_t)HW);
+        // h in the place of the gate accumulators; largest magnitude per row of
+        // this wave's 32 channels, an MXFP8 block: the other formats' 128 are those
+        // of the waves of a row
+        float amax[MT];
 #pragma unroll
         for (int i = 0; i < MT; ++i) {
-            float amax = 0.0f;
+            amax[i] = 0.0f;
 #pragma unroll
             for (int f = 0; f < 2; ++f)
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
                     acc[f][i][j] = dev::swiglu(acc[f][i][j], acc[f + 2][i][j]);
-                    amax = fmaxf(amax, fabsf(acc[f][i][j]));
+                    amax[i] = fmaxf(amax[i], fabsf(acc[f][i][j]));
                 }
-            amax = fmaxf(amax, __shfl_xor(amax, 16));
-            amax = fmaxf(amax, __shfl_xor(amax, 32));
-            if (g == 0)
-                wave_max[wc][(wr * MT + i) * 16 + r] = amax;
+            amax[i] = fmaxf(amax[i], __shfl_xor(amax[i], 16));
+            amax[i] = fmaxf(amax[i], __shfl_xor(amax[i], 32));
+            if (QUANT != MOE_QUANT_MXFP8 && g == 0)
+                wave_max[wc][(wr * MT + i) * 16 + r] = amax[i];
         }
-        __syncthreads();
+        if constexpr (QUANT != MOE_QUANT_MXFP8)
+            meet();
 #pragma unroll
         for (int i = 0; i < MT; ++i) {
             const int32_t row = (wr * MT + i) * 16 + r;
-            float amax = wave_max[wc][row];
             if constexpr (QUANT != MOE_QUANT_MXFP8) {
 #pragma unroll
                 for (int w = 0; w < 4; ++w)
-                    amax = fmaxf(amax, wave_max[w][row]);
+                    amax[i] = fmaxf(amax[i], wave_max[w][row]);
             }
-            const dev::BlockScale<QUANT> bs(amax);
-            if (row < at.valid) {
-                const int64_t grow = at.row0 + row;
+            const dev::BlockScale<QUANT> bs(amax[i]);
+            uint32_t q[2];
 #pragma unroll
-                for (int f = 0; f < 2; ++f)
-                    *reinterpret_cast<uint32_t *>(p.h + grow * inter + at.nt * 128 + wc * 32 + f * 16 + g * 4) =
-                        dev::pack_e4m3(bs.apply(acc[f][i][0]), bs.apply(acc[f][i][1]), bs.apply(acc[f][i][2]),
-                                       bs.apply(acc[f][i][3]));
-                const int HB = inter / kQuantGroup;
-                if constexpr (QUANT == MOE_QUANT_FP8_F32) {
-                    if (wc == 0 && g == 0)
-                        static_cast<float *>(p.h_scale)[grow * HB + at.nt] = bs.s;
-                } else if constexpr (QUANT == MOE_QUANT_FP8_UE8M0) {
-                    const int HW = (HB + 3) / 4 * 4;
-                    uint8_t *sc = static_cast<uint8_t *>(p.h_scale) + grow * HW;
-                    if (wc == 0 && g == 0) {
-                        sc[at.nt] = (uint8_t)bs.byte;
-                        if (at.nt == HB - 1)  // the last word's unused high bytes are 0
-                            for (int b = HB; b < HW; ++b)
-                                sc[b] = 0;
-                    }
-                } else {
-                    if (g == 0)
-                        static_cast<uint8_t *>(p.h_scale)[grow * HB * 4 + at.nt * 4 + wc] = (uint8_t)bs.byte;
-                }
+            for (int f = 0; f < 2; ++f)
+                q[f] = dev::pack_e4m3(bs.apply(acc[f][i][0]), bs.apply(acc[f][i][1]), bs.apply(acc[f][i][2]),
+                                      bs.apply(acc[f][i][3]));
+            // 8 adjacent channels per lane, as above
+            const auto pair = __builtin_amdgcn_permlane16_swap(q[0], q[1], false, false);
+            const uint32_t off = (uint32_t)row * (uint32_t)inter + at.nt * 128 + wc * 32 + (g & 1) * 16 + (g >> 1) * 8;
+            __builtin_amdgcn_raw_buffer_store_b64(dev::u32x2{pair[0], pair[1]}, out,
+                                                  row < at.valid ? off : 0x80000000u, 0, 0);
+            const bool one = row < at.valid && g == 0 && (QUANT == MOE_QUANT_MXFP8 || wc == 0);
+            const uint32_t soff = one ? (uint32_t)row * HW + at.nt * kScale + (QUANT == MOE_QUANT_MXFP8 ? wc : 0)
+                                      : 0x80000000u;
+            if constexpr (QUANT == MOE_QUANT_FP8_F32) {
+                __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(bs.s), scales, soff, 0, 0);
+            } else {
+                __builtin_amdgcn_raw_buffer_store_b8((uint8_t)bs.byte, scales, soff, 0, 0);
+                if constexpr (QUANT == MOE_QUANT_FP8_UE8M0)
+                    if (at.nt == HB - 1)  // the last word's unused high bytes are 0
+                        for (int b = 1; b <= HW - HB; ++b)
+                            __builtin_amdgcn_raw_buffer_store_b8((uint8_t)0, scales, soff, b, 0);
             }
         }
+        store_nothing<kStores(kMaxMT) - kStores(MT)>(out);
     }
 }
 
@@ -234,18 +272,18 @@ __global__ __launch_bounds__(kGemmThreads) void expert_gemm_stream(ExpertGemmArg
     const int KB = p.k / kQuantGroup;
     const int KW = (KB + 3) / 4;
     const int NBn = (p.n + kQuantGroup - 1) / kQuantGroup;
-    scan_tiles<BM, kGemmThreads>(p.recv_count, p.E, p.dense_rows, tile_start, red);
+    scan_tiles<BM, kGemmThreads, 1>(p, tile_start, red);
     const int64_t n_work = (int64_t)scalar(tile_start[p.E]) * n_tiles;
 
     for (int64_t work = blockIdx.x; work < n_work; work += gridDim.x) {
         const int32_t m = (int32_t)(work / n_tiles);
         TileAt at;
         at.nt = scalar((int32_t)(work - (int64_t)m * n_tiles));
-        at.e = scalar(find_expert(tile_start, p.E, m));
-        const int32_t first = scalar((m - tile_start[at.e]) * BM);
-        const int32_t count = p.recv_count != nullptr ? word_of(p.recv_count, at.e) : p.dense_rows;
-        at.valid = min(BM, count - first);
-        at.row0 = (int64_t)(p.recv_count != nullptr ? word_of(p.expert_offset, at.e) : 0) + first;
+        const ExpertAt ex = find_expert<BM, 1>(p, tile_start, m);
+        const int32_t first = (m - ex.start) * BM;
+        at.e = scalar(ex.e);
+        at.valid = scalar(min(BM, ex.rows - first));
+        at.row0 = (int64_t)(p.expert_offset != nullptr ? word_of(p.expert_offset, at.e) : 0) + scalar(first);
 
         const int64_t arow = at.row0 + min(r, at.valid - 1);
         int64_t wrow[kNF], nb[kNF];
@@ -395,15 +433,28 @@ __device__ __forceinline__ void for_each(const F &f)
     }
 }
 
-// One stage in LDS: rows, weights, then scale words, 64 per wave: one per row,
-// then one per channel (MXFP8) or 128-channel block (the first two).
+// One stage in LDS: rows, then weights.
 template <int BM>
 struct Stage {
     static constexpr int kW = BM * kQuantGroup;
-    static constexpr int kSa = kW + kTileN * kQuantGroup;
-    static constexpr int kSw = kSa + BM * 4;
-    static constexpr int kBytes = kSa + kTileWaves * kWave * 4;
-    static constexpr int kLoads = BM / 64 + 4 + 1;  // loads of a wave per stage
+    static constexpr int kBytes = kW + kTileN * kQuantGroup;
+    static constexpr int kLoads = 1 + BM / 64 + 4;  // loads of a wave per step, scales first
+};
+
+// The scales of four blocks in LDS: per row, then per channel (MXFP8) or
+// 128-channel block (the first two), the four blocks' words or their one word
+// of bytes.  A row's scales of one block are a few bytes of a line of their
+// own: read once per four blocks they cost L2 a quarter (MXFP8, gate and up
+// products of 32,768 rows, 64 experts, 7168 -> 2 x 2048: 1465 -> 1141 us).
+// Two chunks take turns; the third place takes what the loads that keep the
+// count (TileLoads::issue) bring.
+template <int QUANT, int BM>
+struct Chunk {
+    static constexpr int kWord = QUANT == MOE_QUANT_FP8_UE8M0 ? 4 : 16;
+    static constexpr int kEntries = BM + (QUANT == MOE_QUANT_MXFP8 ? kTileN : kWave);
+    static constexpr int kBytes = kEntries * kWord;
+    static constexpr int kAll = 2 * kBytes + kWave * kWord;
+    static_assert(kEntries <= kTileThreads, "one load");
 };
 
 // The loads of one tile: descriptors (uniform) and this lane's offsets.
@@ -418,6 +469,7 @@ struct TileLoads {
     __amdgpu_buffer_rsrc_t a, w[2], s;
     uint32_t ao[BM / 64], wo[SWIGLU ? 2 : 4], so;  // rows, weights (both halves alike with SWIGLU), scales
     int KB, wave;
+    using C = Chunk<QUANT, BM>;
 
     __device__ __forceinline__ void set(const ExpertGemmArgs &p, const TileAt &at, int wave_, int lane)
     {
@@ -444,8 +496,7 @@ struct TileLoads {
             for (int i = 0; i < 2; ++i)
                 wo[SWIGLU ? i : 2 * h + i] = (uint32_t)min(row + 64 * i, left - 1) * k + piece;
         }
-        // scales: the first BM / 64 waves load the rows' words, the others the weights'
-        static_assert(QUANT != MOE_QUANT_MXFP8 || BM <= 256, "MXFP8 needs four waves for the channels' words");
+        // scales: the first BM / 64 waves load the rows', the others the weights'
         const bool of_rows = wave < BM / kWave;
         const int t = (of_rows ? wave : wave - BM / kWave) * kWave + lane;
         const int32_t w_rows = QUANT == MOE_QUANT_MXFP8 ? p.n : NBn;
@@ -458,26 +509,32 @@ struct TileLoads {
         s = buffer(static_cast<const uint32_t *>(src) + first * SW, (uint32_t)rows * SW * 4);
         so = (uint32_t)min(of_rows ? t : w_row, rows - 1) * SW * 4;
     }
-    // Loads FROM .. TO - 1 of block kb into a stage; the blocks after the last
-    // are asked for past the buffers' ends, which costs no memory access.
+    // Loads FROM .. TO - 1 of step `at` (NS - 1 blocks before `kb`): block kb into a
+    // stage and, every fourth step, the scales of the next four blocks into
+    // the chunk that is not in use.  The blocks after the last are asked for
+    // past the buffers' ends, which costs no memory access, and so are scales in
+    // the other steps: every step has the same number of loads.
     template <int FROM, int TO>
-    __device__ __forceinline__ void issue(uint8_t *st, int kb) const
+    __device__ __forceinline__ void issue(uint8_t *st, int kb, uint8_t *chunks, int at) const
     {
         constexpr int kA = BM / 64;
         const uint32_t past = kb < KB ? 0u : 0x80000000u;
-        const int b = kb < KB ? kb : 0;
-        const uint32_t at_k = (uint32_t)b * kQuantGroup;
+        const uint32_t at_k = kb < KB ? (uint32_t)kb * kQuantGroup : 0u;
 #pragma unroll
         for (int j = FROM; j < TO; ++j) {
-            if (j < kA) {
-                load_lds<16>(a, st + (wave + 8 * j) * 1024, ao[j] | past, at_k);
-            } else if (j < kA + 4) {
-                const int i = j - kA;
+            if (j == 0) {
+                const int c = (at >> 2) + 1;
+                const bool turn = (at & 3) == 0 && wave < C::kEntries / kWave, some = turn && 4 * c < KB;
+                const uint32_t to = turn ? (uint32_t)((c & 1) * C::kBytes + wave * kWave * C::kWord) : 2 * C::kBytes;
+                load_lds<C::kWord>(s, chunks + to, so | (some ? 0u : 0x80000000u),
+                                   some ? (uint32_t)c * C::kWord : 0u);
+            } else if (j < 1 + kA) {
+                const int i = j - 1;
+                load_lds<16>(a, st + (wave + 8 * i) * 1024, ao[i] | past, at_k);
+            } else {
+                const int i = j - 1 - kA;
                 load_lds<16>(w[i >> 1], st + Stage<BM>::kW + (wave + 8 * i) * 1024, wo[SWIGLU ? i & 1 : i] | past,
                              at_k);
-            } else {
-                const uint32_t word = QUANT == MOE_QUANT_FP8_UE8M0 ? (uint32_t)b >> 2 : (uint32_t)b;
-                load_lds<4>(s, st + Stage<BM>::kSa + wave * 256, so | past, word * 4);
             }
         }
     }
@@ -494,24 +551,25 @@ struct TileLoads {
 // stays near 1e-8 at half the rate.
 template <int QUANT, bool SWIGLU, int BM, int MT, bool EXACT>
 __device__ __forceinline__ void multiply_stage(dev::f32x4 (&acc)[kNF][MT], const uint8_t *st, int wr, int wc, int lane,
-                                               int u, const TileLoads<QUANT, SWIGLU, BM> &loads, uint8_t *free,
-                                               int kb_load)
+                                               const TileLoads<QUANT, SWIGLU, BM> &loads, uint8_t *free, int kb_load,
+                                               uint8_t *chunks, int kb)
 {
+    using C = Chunk<QUANT, BM>;
     constexpr int kLoads = Stage<BM>::kLoads;
     const int r = lane & 15, g = lane >> 4;
     const int rswz = (r >> 1) & 7;
     const int rlo = r * kQuantGroup + ((g ^ rswz) * 16), rhi = r * kQuantGroup + (((4 + g) ^ rswz) * 16);
     const uint8_t *rows = st + wr * MT * 16 * kQuantGroup;
-    const uint32_t *sa = reinterpret_cast<const uint32_t *>(st + Stage<BM>::kSa) + wr * MT * 16 + r;
-    const uint32_t *sw = reinterpret_cast<const uint32_t *>(st + Stage<BM>::kSw);
+    const int u = kb & 3;
+    const uint8_t *sc = chunks + ((kb >> 2) & 1) * C::kBytes + (QUANT == MOE_QUANT_FP8_UE8M0 ? 0 : 4 * u);
+    const auto scale = [&](int entry) { return *reinterpret_cast<const uint32_t *>(sc + entry * C::kWord); };
     dev::i32x8 w[kNF], x[2];
-    uint32_t sx[2];
+    uint32_t sx[MT];
     int swb[kNF];
     float swf[2];
     const auto read_row = [&](int i) {
         x[i & 1] = join(*reinterpret_cast<const dev::u32x4 *>(rows + rlo + i * 16 * kQuantGroup),
                         *reinterpret_cast<const dev::u32x4 *>(rows + rhi + i * 16 * kQuantGroup));
-        sx[i & 1] = sa[i * 16];
     };
 #pragma unroll
     for (int f = 0; f < kNF; ++f) {
@@ -519,24 +577,30 @@ __device__ __forceinline__ void multiply_stage(dev::f32x4 (&acc)[kNF][MT], const
         const uint8_t *src = st + Stage<BM>::kW + c * kQuantGroup;
         w[f] = join(*reinterpret_cast<const dev::u32x4 *>(src + rlo), *reinterpret_cast<const dev::u32x4 *>(src + rhi));
         if constexpr (QUANT == MOE_QUANT_MXFP8)
-            swb[f] = (int)(sw[c + r] >> (8 * g));
-        if (f == 0)
+            swb[f] = (int)(scale(BM + c + r) >> (8 * g));
+        if (f == 0) {
             read_row(0);
+            // all scales before this step's load of scales: the compiler has reads
+            // of the chunks wait for the last load into them
+#pragma unroll
+            for (int i = 0; i < MT; ++i)
+                sx[i] = scale((wr * MT + i) * 16 + r);
+        }
     }
     if constexpr (QUANT == MOE_QUANT_FP8_F32) {
-        swf[0] = __uint_as_float(sw[SWIGLU ? 0 : wc >> 1]);
-        swf[1] = SWIGLU ? __uint_as_float(sw[1]) : swf[0];
+        swf[0] = __uint_as_float(scale(BM + (SWIGLU ? 0 : wc >> 1)));
+        swf[1] = SWIGLU ? __uint_as_float(scale(BM + 1)) : swf[0];
     } else if constexpr (QUANT == MOE_QUANT_FP8_UE8M0) {
-        swb[0] = swb[1] = (int)(sw[SWIGLU ? 0 : wc >> 1] >> (8 * u));
-        swb[2] = swb[3] = SWIGLU ? (int)(sw[1] >> (8 * u)) : swb[0];
+        swb[0] = swb[1] = (int)(scale(BM + (SWIGLU ? 0 : wc >> 1)) >> (8 * u));
+        swb[2] = swb[3] = SWIGLU ? (int)(scale(BM + 1) >> (8 * u)) : swb[0];
     }
     const auto part = [&](auto I) {
         constexpr int i = decltype(I)::value;
         if constexpr (i + 1 < MT)
             read_row(i + 1);
         if constexpr (QUANT == MOE_QUANT_FP8_F32) {
-            const float s0 = __uint_as_float(sx[i & 1]) * swf[0];
-            const float s1 = SWIGLU ? __uint_as_float(sx[i & 1]) * swf[1] : s0;
+            const float s0 = __uint_as_float(sx[i]) * swf[0];
+            const float s1 = SWIGLU ? __uint_as_float(sx[i]) * swf[1] : s0;
             dev::f32x4 d[kNF];
             dev::bf16x8 xv[4];
             if constexpr (EXACT)
@@ -555,19 +619,19 @@ __device__ __forceinline__ void multiply_stage(dev::f32x4 (&acc)[kNF][MT], const
                     d[f] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(w[f], x[i & 1], z, 0, 0, 0, 0, 0, 0);
                 }
             }
-            loads.template issue<i * kLoads / MT, (i + 1) * kLoads / MT>(free, kb_load);
+            loads.template issue<i * kLoads / MT, (i + 1) * kLoads / MT>(free, kb_load, chunks, kb);
 #pragma unroll
             for (int f = 0; f < kNF; ++f)
 #pragma unroll
                 for (int j = 0; j < 4; ++j)
                     acc[f][i][j] = __builtin_fmaf(d[f][j], f < 2 ? s0 : s1, acc[f][i][j]);
         } else {
-            const int sb = (int)(sx[i & 1] >> (8 * (QUANT == MOE_QUANT_FP8_UE8M0 ? u : g)));
+            const int sb = (int)(sx[i] >> (8 * (QUANT == MOE_QUANT_FP8_UE8M0 ? u : g)));
 #pragma unroll
             for (int f = 0; f < kNF; ++f)
                 acc[f][i] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(w[f], x[i & 1], acc[f][i], 0, 0, 0,
                                                                               swb[f], 0, sb);
-            loads.template issue<i * kLoads / MT, (i + 1) * kLoads / MT>(free, kb_load);
+            loads.template issue<i * kLoads / MT, (i + 1) * kLoads / MT>(free, kb_load, chunks, kb);
         }
         __builtin_amdgcn_sched_barrier(0);
     };
@@ -577,20 +641,21 @@ __device__ __forceinline__ void multiply_stage(dev::f32x4 (&acc)[kNF][MT], const
 // Starts the loads of a tile's first NS - 1 stages.
 template <int QUANT, bool SWIGLU, int BM, int NS>
 __device__ __forceinline__ void start_tile(const ExpertGemmArgs &p, const TileAt &at, uint8_t *st0, uint8_t *st1,
-                                           int wave, int lane)
+                                           uint8_t *chunks, int wave, int lane)
 {
     TileLoads<QUANT, SWIGLU, BM> loads;
     loads.set(p, at, wave, lane);
-    loads.template issue<0, Stage<BM>::kLoads>(st0, 0);
+    loads.template issue<0, Stage<BM>::kLoads>(st0, 0, chunks, -4);
     if constexpr (NS == 3)
-        loads.template issue<0, Stage<BM>::kLoads>(st1, 1);
+        loads.template issue<0, Stage<BM>::kLoads>(st1, 1, chunks, -3);
 }
 
 // Multiplies a tile whose first NS - 1 stages are in flight, then starts the
 // next tile's (`more`) and writes the results.
 template <int QUANT, bool SWIGLU, int BM, int NS, int MT>
 __device__ __forceinline__ void run_tile(const ExpertGemmArgs &p, const TileAt &at, const TileAt &next, bool more,
-                                         uint8_t *st0, uint8_t *st1, uint8_t *st2, int wave, int lane)
+                                         uint8_t *st0, uint8_t *st1, uint8_t *st2, uint8_t *chunks,
+                                         float (*wave_max)[BM], int wave, int lane)
 {
     TileLoads<QUANT, SWIGLU, BM> loads;
     loads.set(p, at, wave, lane);
@@ -606,9 +671,9 @@ __device__ __forceinline__ void run_tile(const ExpertGemmArgs &p, const TileAt &
     // FIRST: the stores of the tile before may still be on their way, behind the
     // loads of this tile's first NS - 1 stages
     const auto step = [&](auto first, auto exact, uint8_t *cur, uint8_t *free, int kb) {
-        wait_and_meet<kAhead + (decltype(first)::value && !SWIGLU ? kTileStores(BM) : 0)>();
-        multiply_stage<QUANT, SWIGLU, BM, MT, decltype(exact)::value>(acc, cur, wr, wc, lane, kb & 3, loads, free,
-                                                                      kb + NS - 1);
+        wait_and_meet<kAhead + (decltype(first)::value ? kStores(BM / 32) : 0)>();
+        multiply_stage<QUANT, SWIGLU, BM, MT, decltype(exact)::value>(acc, cur, wr, wc, lane, loads, free,
+                                                                      kb + NS - 1, chunks, kb);
     };
     // The fp32 scales of SwiGLU's output would show the 8-bit instruction's error
     // (1.15e-5 rms of them): every third block goes through bf16 operands, which
@@ -646,24 +711,26 @@ __device__ __forceinline__ void run_tile(const ExpertGemmArgs &p, const TileAt &
     }
     wait_and_meet<0>();
     if (more)
-        start_tile<QUANT, SWIGLU, BM, NS>(p, next.scalars(), st0, st1, wave, lane);
-    // the stage that the next tile's loads leave alone holds the rows' maxima
-    write_tile<QUANT, MT, SWIGLU, BM>(p, acc, at, wr, wc, lane, reinterpret_cast<float(*)[BM]>(NS == 3 ? st2 : st1));
+        start_tile<QUANT, SWIGLU, BM, NS>(p, next.scalars(), st0, st1, chunks, wave, lane);
+    write_tile<QUANT, MT, SWIGLU, BM>(p, acc, at, wr, wc, lane, wave_max);
 }
 
 template <int QUANT, bool SWIGLU, int BM, int NS>
 __global__ __launch_bounds__(kTileThreads) void expert_gemm_tiles(ExpertGemmArgs p, int32_t n_tiles)
 {
-    __shared__ int32_t tile_start[kMaxExperts + 1];
+    constexpr int kGroup = 4;  // a whole table of the experts would not fit
+    __shared__ int32_t tile_start[kMaxExperts / kGroup + 1];
     __shared__ int32_t red[kTileWaves];
     // separate variables: the compiler then knows which reads follow which loads
     __shared__ alignas(1024) uint8_t st0[Stage<BM>::kBytes];
     __shared__ alignas(1024) uint8_t st1[Stage<BM>::kBytes];
     __shared__ alignas(1024) uint8_t st2[NS == 3 ? Stage<BM>::kBytes : 16];
+    __shared__ alignas(16) uint8_t chunks[Chunk<QUANT, BM>::kAll];
+    __shared__ float wave_max[SWIGLU && QUANT != MOE_QUANT_MXFP8 ? kWaveCols : 1][BM];
     const int lane = threadIdx.x & (kWave - 1);
     const int wave = scalar(threadIdx.x / kWave);
-    scan_tiles<BM, kTileThreads>(p.recv_count, p.E, p.dense_rows, tile_start, red);
-    const int64_t n_work = (int64_t)scalar(tile_start[p.E]) * n_tiles;
+    scan_tiles<BM, kTileThreads, kGroup>(p, tile_start, red);
+    const int64_t n_work = (int64_t)scalar(tile_start[(p.E + kGroup - 1) / kGroup]) * n_tiles;
     // workgroups go to the 8 XCDs in turn: each XCD takes a contiguous run of
     // the work, so that the tiles of one expert share its L2
     const int64_t run = (n_work + 7) / 8;
@@ -675,28 +742,26 @@ __global__ __launch_bounds__(kTileThreads) void expert_gemm_tiles(ExpertGemmArgs
     const auto locate = [&](int64_t idx) {
         const int64_t work = base + idx;
         TileAt at;
-        at.e = scalar(find_expert(tile_start, p.E, (int32_t)(work / n_tiles)));
-        const int32_t e_first = scalar(tile_start[at.e]);
-        const int32_t e_tiles = scalar(tile_start[at.e + 1]) - e_first;
-        const int64_t local = work - (int64_t)e_first * n_tiles;
+        const ExpertAt ex = find_expert<BM, kGroup>(p, tile_start, scalar((int32_t)(work / n_tiles)));
+        const int32_t e_tiles = (ex.rows + BM - 1) / BM;
+        const int64_t local = work - (int64_t)ex.start * n_tiles;
         const int32_t grp = (int32_t)(local / ((int64_t)kMGroup * n_tiles));
         const int32_t in_grp = (int32_t)(local - (int64_t)grp * kMGroup * n_tiles);
         const int32_t grp_rows = min(kMGroup, e_tiles - grp * kMGroup);
+        at.e = scalar(ex.e);
         at.nt = scalar(in_grp / grp_rows);
         const int32_t first = scalar((grp * kMGroup + in_grp % grp_rows) * BM);
-        const int32_t count = p.recv_count != nullptr ? word_of(p.recv_count, at.e) : p.dense_rows;
-        const int32_t seg = p.recv_count != nullptr ? word_of(p.expert_offset, at.e) : 0;
-        at.valid = min(BM, count - first);
-        at.row0 = (int64_t)seg + first;
+        at.valid = scalar(min(BM, ex.rows - first));
+        at.row0 = (int64_t)(p.expert_offset != nullptr ? word_of(p.expert_offset, at.e) : 0) + first;
         return at;
     };
     int64_t idx = blockIdx.x >> 3;
     if (idx >= end)
         return;
     TileAt next = locate(idx);
-    start_tile<QUANT, SWIGLU, BM, NS>(p, next, st0, st1, wave, lane);
-    if constexpr (!SWIGLU)  // as many as behind the loads of every later tile (see step)
-        store_nothing<kTileStores(BM)>(buffer(p.y, 0));
+    start_tile<QUANT, SWIGLU, BM, NS>(p, next, st0, st1, chunks, wave, lane);
+    // as many as behind the loads of every later tile (see step)
+    store_nothing<kStores(BM / 32)>(buffer(p.a, 0));
     for (;;) {
         const TileAt at = next.scalars();
         idx += gridDim.x >> 3;
@@ -706,11 +771,11 @@ __global__ __launch_bounds__(kTileThreads) void expert_gemm_tiles(ExpertGemmArgs
         // a tile that is not full takes the code for its size
         constexpr int MT = BM / 16 / kWaveRows, M2 = (MT + 1) / 2, M1 = (MT + 3) / 4;
         if (at.valid > M2 * 32)
-            run_tile<QUANT, SWIGLU, BM, NS, MT>(p, at, next, more, st0, st1, st2, wave, lane);
+            run_tile<QUANT, SWIGLU, BM, NS, MT>(p, at, next, more, st0, st1, st2, chunks, wave_max, wave, lane);
         else if (at.valid > M1 * 32)
-            run_tile<QUANT, SWIGLU, BM, NS, M2>(p, at, next, more, st0, st1, st2, wave, lane);
+            run_tile<QUANT, SWIGLU, BM, NS, M2>(p, at, next, more, st0, st1, st2, chunks, wave_max, wave, lane);
         else
-            run_tile<QUANT, SWIGLU, BM, NS, M1>(p, at, next, more, st0, st1, st2, wave, lane);
+            run_tile<QUANT, SWIGLU, BM, NS, M1>(p, at, next, more, st0, st1, st2, chunks, wave_max, wave, lane);
         if (!more)
             break;
     }

@@ -8,24 +8,13 @@
 namespace moe {
 namespace dev {
 
+typedef unsigned int u32x2 __attribute__((ext_vector_type(2)));
 typedef int i32x8 __attribute__((ext_vector_type(8)));
-typedef int i32x4 __attribute__((ext_vector_type(4)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 
 constexpr bool per_row_weight_scale(int quant) { return quant == MOE_QUANT_MXFP8; }
-
-// One operand of v_mfma_f32_16x16x128_f8f6f4: lane l holds row (l & 15), and of
-// that row's 128 channels the 16 bytes at 16 * (l >> 4) and at 64 + 16 * (l >> 4)
-// -- the order in which the instruction counts channels, and in memory two
-// loads that cover 64 contiguous bytes of each of 16 rows.
-__device__ __forceinline__ i32x8 load_frag(const uint8_t *row_k, int g)
-{
-    const u32x4 lo = *reinterpret_cast<const u32x4 *>(row_k + 16 * g);
-    const u32x4 hi = *reinterpret_cast<const u32x4 *>(row_k + 64 + 16 * g);
-    return i32x8{(int)lo[0], (int)lo[1], (int)lo[2], (int)lo[3], (int)hi[0], (int)hi[1], (int)hi[2], (int)hi[3]};
-}
 
 // fp32 -> bf16 bits, round to nearest even (finite values and infinities).
 __device__ __forceinline__ uint32_t bf16_bits(float f)
