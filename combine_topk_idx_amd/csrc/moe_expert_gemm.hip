@@ -164,13 +164,19 @@ __device__ __forceinline__ void write_tile(const ExpertGemmArgs &p, dev::f32x4 (
     const int r = lane & 15, g = lane >> 4;
     if constexpr (!SWIGLU) {
         // Two fragments' results change places between odd and even rows of 16
-        // lanes: a lane then has 8 adjacent channels of its row, and a store covers
-        // 64 bytes of each of 16 rows.  Rows and channels past the end go past the
-        // buffer's: every wave issues the same number of stores.
+        // lanes: a lane then has 8 adjacent channels of its row, and 4 lanes half of
+        // the row's 64.  The other half comes from the lane 8 further, for the
+        // half that one needs: a store then covers whole cache lines, 128 bytes of
+        // each of 8 rows.  Rows and channels past the end go past the buffer's:
+        // every wave issues the same number of stores.  Large tiles' stores are
+        // marked as streamed (non-temporal), which leaves L2 to the weights (8192
+        // dense rows, 7168 -> 8192, UE8M0: 424 -> 382 us).
+        constexpr int kStreamed = BM <= 16 ? 0 : 2;
         const __amdgpu_buffer_rsrc_t out = buffer(p.y + at.row0 * p.n, (uint32_t)at.valid * (uint32_t)p.n * 2);
+        const bool low = r < 8;
 #pragma unroll
         for (int i = 0; i < MT; ++i) {
-            const int32_t row = (wr * MT + i) * 16 + r;
+            dev::u32x4 v[2];
 #pragma unroll
             for (int f = 0; f < kNF; f += 2) {
                 const auto lo = __builtin_amdgcn_permlane16_swap(dev::pack_bf16(acc[f][i][0], acc[f][i][1]),
@@ -179,10 +185,20 @@ __device__ __forceinline__ void write_tile(const ExpertGemmArgs &p, dev::f32x4 (
                 const auto hi = __builtin_amdgcn_permlane16_swap(dev::pack_bf16(acc[f][i][2], acc[f][i][3]),
                                                                  dev::pack_bf16(acc[f + 1][i][2], acc[f + 1][i][3]),
                                                                  false, false);
-                const int32_t n = at.nt * kTileN + wc * 64 + (f + (g & 1)) * 16 + (g >> 1) * 8;
+                v[f / 2] = dev::u32x4{lo[0], hi[0], lo[1], hi[1]};
+            }
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const uint32_t other = __builtin_amdgcn_update_dpp(0, low ? v[1][j] : v[0][j], 0x128, 0xF, 0xF, true);
+                v[0][j] = low ? v[0][j] : other;
+                v[1][j] = low ? other : v[1][j];
+            }
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const int32_t row = (wr * MT + i) * 16 + h * 8 + (r & 7);
+                const int32_t n = at.nt * kTileN + wc * 64 + (low ? 0 : 32) + (g & 1) * 16 + (g >> 1) * 8;
                 const uint32_t off = row < at.valid && n < p.n ? ((uint32_t)row * (uint32_t)p.n + n) * 2 : 0x80000000u;
-                const dev::u32x4 v = {lo[0], hi[0], lo[1], hi[1]};
-                __builtin_amdgcn_raw_buffer_store_b128(v, out, off, 0, 0);
+                __builtin_amdgcn_raw_buffer_store_b128(v[h], out, off, 0, kStreamed);
             }
         }
         store_nothing<kStores(kMaxMT) - kStores(MT)>(out);
@@ -815,10 +831,10 @@ hipError_t launch_rows(const ExpertGemmArgs &p, hipStream_t stream)
     const int64_t per_expert = p.max_rows / p.E;
     if (per_expert <= 16)
         return launch_stream<QUANT, SWIGLU>(p, stream);
-    if constexpr (QUANT != MOE_QUANT_FP8_F32 || !SWIGLU) {
+    if constexpr (!SWIGLU) {
         const int64_t parts = p.max_rows < p.E ? p.max_rows : p.E;
         const int64_t tiles = (p.max_rows / 256 + parts) * ((p.n + kTileN - 1) / kTileN);
-        if (per_expert > 512 && tiles >= device_cu_count())
+        if (per_expert >= 512 && tiles >= device_cu_count())
             return launch_tiles<QUANT, SWIGLU, 256, 2>(p, stream);
     }
     return launch_tiles<QUANT, SWIGLU, 128, 3>(p, stream);
