@@ -18,10 +18,13 @@ namespace moe {
 
 namespace {
 
-constexpr int kGemmThreads = 256;
-constexpr int kGemmWaves = kGemmThreads / kWave;
+constexpr int kTileThreads = 512;
+constexpr int kTileWaves = kTileThreads / kWave;
+constexpr int kWaveRows = 2, kWaveCols = 4;   // waves over the tile's rows and channels
 constexpr int kNF = 4;                        // 16-channel fragments per wave
-constexpr int kTileN = kGemmWaves * kNF * 16;  // output channels per block
+constexpr int kTileN = kWaveCols * kNF * 16;  // output channels per block
+constexpr int kMGroup = 8;                    // row tiles that walk the channel tiles together
+constexpr int kGroup = 4;                     // experts per entry of a block's table of tiles
 
 // A value that is the same in every lane, in a scalar register.  Where the
 // compiler can tell that it is, it drops a plain readfirstlane, may keep the
@@ -41,15 +44,16 @@ __device__ __forceinline__ int32_t word_of(const int32_t *a, int32_t i)
     return reinterpret_cast<const __attribute__((address_space(4))) int32_t *>((uint64_t)a)[i];
 }
 
-// tile_start[i] = row tiles of BM rows before expert G i; [ceil(E / G)] = all.
-// Block-wide, ends with a barrier.
-template <int BM, int NT, int G>
+// tile_start[i] = row tiles of BM rows before expert kGroup i, [ceil(E / kGroup)]
+// = all: a table of every expert would not fit beside the stages.  Block-wide,
+// ends with a barrier.
+template <int BM>
 __device__ inline void scan_tiles(const ExpertGemmArgs &p, int32_t *tile_start, int32_t *red)
 {
     const int tid = threadIdx.x, lane = tid & (kWave - 1), wave = tid / kWave;
-    const int groups = (p.E + G - 1) / G;
-    const int per = (groups + NT - 1) / NT;
-    const int e0 = min(groups, tid * per) * G, e1 = min(groups, (tid + 1) * per) * G;
+    const int groups = (p.E + kGroup - 1) / kGroup;
+    const int per = (groups + kTileThreads - 1) / kTileThreads;
+    const int e0 = min(groups, tid * per) * kGroup, e1 = min(groups, (tid + 1) * per) * kGroup;
     const auto tiles = [&](int e) {
         return ((e >= p.E ? 0 : p.recv_count != nullptr ? p.recv_count[e] : p.dense_rows) + BM - 1) / BM;
     };
@@ -60,13 +64,13 @@ __device__ inline void scan_tiles(const ExpertGemmArgs &p, int32_t *tile_start, 
     if (lane == kWave - 1)
         red[wave] = incl;
     __syncthreads();
-    int32_t run = dev::sum_before<NT / kWave>(red, wave) + incl - local;
+    int32_t run = dev::sum_before<kTileWaves>(red, wave) + incl - local;
     for (int e = e0; e < e1; ++e) {
-        if (e % G == 0)
-            tile_start[e / G] = run;
+        if (e % kGroup == 0)
+            tile_start[e / kGroup] = run;
         run += tiles(e);
     }
-    if (tid == NT - 1)
+    if (tid == kTileThreads - 1)
         tile_start[groups] = run;
     __syncthreads();
 }
@@ -78,10 +82,10 @@ struct ExpertAt {
 };
 
 // The expert that row tile m (uniform, below the number of all) belongs to.
-template <int BM, int G>
+template <int BM>
 __device__ __forceinline__ ExpertAt find_expert(const ExpertGemmArgs &p, const int32_t *tile_start, int32_t m)
 {
-    int lo = 0, hi = (p.E + G - 1) / G;
+    int lo = 0, hi = (p.E + kGroup - 1) / kGroup;
     while (hi - lo > 1) {
         const int mid = (lo + hi) >> 1;
         if (scalar(tile_start[mid]) <= m)
@@ -91,16 +95,16 @@ __device__ __forceinline__ ExpertAt find_expert(const ExpertGemmArgs &p, const i
     }
     if (p.recv_count == nullptr)
         return ExpertAt{0, 0, p.dense_rows};
-    int32_t rows[G];
+    int32_t rows[kGroup];
 #pragma unroll
-    for (int i = 0; i < G; ++i)
-        rows[i] = word_of(p.recv_count, min(lo * G + i, p.E - 1));
-    ExpertAt at = {lo * G, scalar(tile_start[lo]), rows[0]};
+    for (int i = 0; i < kGroup; ++i)
+        rows[i] = word_of(p.recv_count, min(lo * kGroup + i, p.E - 1));
+    ExpertAt at = {lo * kGroup, scalar(tile_start[lo]), rows[0]};
 #pragma unroll
-    for (int i = 1; i < G; ++i) {
+    for (int i = 1; i < kGroup; ++i) {
         const int32_t after = at.start + (at.rows + BM - 1) / BM;
         if (m >= after)
-            at = ExpertAt{lo * G + i, after, rows[i]};
+            at = ExpertAt{lo * kGroup + i, after, rows[i]};
     }
     return at;
 }
@@ -160,7 +164,7 @@ template <int QUANT, int MT, bool SWIGLU, int BM>
 __device__ __forceinline__ void write_tile(const ExpertGemmArgs &p, dev::f32x4 (&acc)[kNF][MT], const TileAt &at,
                                            int wr, int wc, int lane, float (*wave_max)[BM])
 {
-    constexpr int kMaxMT = BM <= 16 ? 1 : BM / 32;
+    constexpr int kMaxMT = BM / 32;
     const int r = lane & 15, g = lane >> 4;
     if constexpr (!SWIGLU) {
         // Two fragments' results change places between odd and even rows of 16
@@ -168,10 +172,9 @@ __device__ __forceinline__ void write_tile(const ExpertGemmArgs &p, dev::f32x4 (
         // the row's 64.  The other half comes from the lane 8 further, for the
         // half that one needs: a store then covers whole cache lines, 128 bytes of
         // each of 8 rows.  Rows and channels past the end go past the buffer's:
-        // every wave issues the same number of stores.  Large tiles' stores are
-        // marked as streamed (non-temporal), which leaves L2 to the weights (8192
+        // every wave issues the same number of stores.  They are marked as streamed (non-temporal), which leaves L2 to the weights (8192
         // dense rows, 7168 -> 8192, UE8M0: 424 -> 382 us).
-        constexpr int kStreamed = BM <= 16 ? 0 : 2;
+        constexpr int kStreamed = 2;
         const __amdgpu_buffer_rsrc_t out = buffer(p.y + at.row0 * p.n, (uint32_t)at.valid * (uint32_t)p.n * 2);
         const bool low = r < 8;
 #pragma unroll
@@ -267,136 +270,6 @@ __device__ __forceinline__ void write_tile(const ExpertGemmArgs &p, dev::f32x4 (
 }
 
 // ---------------------------------------------------------------------------
-// Few rows per expert: 16 rows x 256 channels per block of 4 waves.
-//
-// Bound by the weights' bytes: a wave streams its own 64 channels straight to
-// registers, the next block's loads in flight while one is multiplied, with no
-// barrier in the loop; the rows come from L2.  SwiGLU goes through bf16
-// operands (see multiply_stage), whose conversions are free here.
-// ---------------------------------------------------------------------------
-
-template <int QUANT, bool SWIGLU>
-__global__ __launch_bounds__(kGemmThreads) void expert_gemm_stream(ExpertGemmArgs p, int32_t n_tiles)
-{
-    constexpr int BM = 16;
-    __shared__ int32_t tile_start[kMaxExperts + 1];
-    __shared__ int32_t red[kGemmWaves];
-    __shared__ float wave_max[kGemmWaves][BM];
-    const int lane = threadIdx.x & (kWave - 1);
-    const int wave = scalar(threadIdx.x / kWave);
-    const int r = lane & 15, g = lane >> 4;
-    const int KB = p.k / kQuantGroup;
-    const int KW = (KB + 3) / 4;
-    const int NBn = (p.n + kQuantGroup - 1) / kQuantGroup;
-    scan_tiles<BM, kGemmThreads, 1>(p, tile_start, red);
-    const int64_t n_work = (int64_t)scalar(tile_start[p.E]) * n_tiles;
-
-    for (int64_t work = blockIdx.x; work < n_work; work += gridDim.x) {
-        const int32_t m = (int32_t)(work / n_tiles);
-        TileAt at;
-        at.nt = scalar((int32_t)(work - (int64_t)m * n_tiles));
-        const ExpertAt ex = find_expert<BM, 1>(p, tile_start, m);
-        const int32_t first = (m - ex.start) * BM;
-        at.e = scalar(ex.e);
-        at.valid = scalar(min(BM, ex.rows - first));
-        at.row0 = (int64_t)(p.expert_offset != nullptr ? word_of(p.expert_offset, at.e) : 0) + scalar(first);
-
-        const int64_t arow = at.row0 + min(r, at.valid - 1);
-        int64_t wrow[kNF], nb[kNF];
-#pragma unroll
-        for (int f = 0; f < kNF; ++f) {
-            const int32_t c = SWIGLU ? at.nt * 128 + wave * 32 + (f & 1) * 16 + (f >= 2 ? p.n / 2 : 0)
-                                     : at.nt * kTileN + wave * 64 + f * 16;
-            wrow[f] = (int64_t)at.e * p.n + min(c + r, p.n - 1);
-            nb[f] = (int64_t)at.e * NBn + min(c, p.n - 1) / kQuantGroup;
-        }
-        dev::f32x4 acc[kNF][1];
-#pragma unroll
-        for (int f = 0; f < kNF; ++f)
-            acc[f][0] = dev::f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-
-        struct Stage {
-            dev::u32x4 w[kNF][2], x[2];
-            uint32_t sw[kNF], sx;  // scales as they are stored
-        };
-        const auto fill = [&](Stage &st, int kb) {
-            const int64_t at_k = (int64_t)kb * kQuantGroup + 16 * g;
-#pragma unroll
-            for (int f = 0; f < kNF; ++f) {
-                const uint8_t *src = p.w + wrow[f] * p.k + at_k;
-                st.w[f][0] = *reinterpret_cast<const dev::u32x4 *>(src);
-                st.w[f][1] = *reinterpret_cast<const dev::u32x4 *>(src + 64);
-                if constexpr (QUANT == MOE_QUANT_FP8_UE8M0)
-                    st.sw[f] = static_cast<const uint8_t *>(p.w_scale)[nb[f] * KW * 4 + kb];
-                else
-                    st.sw[f] = static_cast<const uint32_t *>(
-                        p.w_scale)[(QUANT == MOE_QUANT_FP8_F32 ? nb[f] : wrow[f]) * KB + kb];
-            }
-            const uint8_t *src = p.a + arow * p.k + at_k;
-            st.x[0] = *reinterpret_cast<const dev::u32x4 *>(src);
-            st.x[1] = *reinterpret_cast<const dev::u32x4 *>(src + 64);
-            if constexpr (QUANT == MOE_QUANT_FP8_UE8M0)
-                st.sx = static_cast<const uint8_t *>(p.a_scale)[arow * KW * 4 + kb];
-            else
-                st.sx = static_cast<const uint32_t *>(p.a_scale)[arow * KB + kb];
-            __builtin_amdgcn_sched_barrier(0);
-        };
-        const auto use = [&](const Stage &st) {
-            const dev::f32x4 z = {0.0f, 0.0f, 0.0f, 0.0f};
-            dev::bf16x8 xv[4];
-            if constexpr (SWIGLU)
-                dev::block_to_bf16<QUANT>(st.x[0], st.x[1], st.sx, g, xv);
-#pragma unroll
-            for (int f = 0; f < kNF; ++f) {
-                dev::f32x4 d = QUANT == MOE_QUANT_FP8_F32 ? z : acc[f][0];
-                if constexpr (SWIGLU) {
-                    dev::bf16x8 wv[4];
-                    dev::block_to_bf16<QUANT>(st.w[f][0], st.w[f][1], st.sw[f], g, wv);
-#pragma unroll
-                    for (int j = 0; j < 4; ++j)
-                        d = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wv[j], xv[j], d, 0, 0, 0);
-                } else if constexpr (QUANT == MOE_QUANT_FP8_F32) {
-                    d = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
-                        join(st.w[f][0], st.w[f][1]), join(st.x[0], st.x[1]), d, 0, 0, 0, 0, 0, 0);
-                } else {
-                    const int shift = QUANT == MOE_QUANT_MXFP8 ? 8 * g : 0;
-                    d = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
-                        join(st.w[f][0], st.w[f][1]), join(st.x[0], st.x[1]), d, 0, 0, 0, (int)(st.sw[f] >> shift), 0,
-                        (int)(st.sx >> shift));
-                }
-                if constexpr (QUANT == MOE_QUANT_FP8_F32) {
-                    const float s = __uint_as_float(st.sx) * __uint_as_float(st.sw[f]);
-#pragma unroll
-                    for (int j = 0; j < 4; ++j)
-                        acc[f][0][j] = __builtin_fmaf(d[j], s, acc[f][0][j]);
-                } else {
-                    acc[f][0] = d;
-                }
-            }
-            __builtin_amdgcn_sched_barrier(0);
-        };
-        Stage s0, s1;
-        int kb = 0;
-        fill(s0, 0);
-        for (; kb + 2 < KB; kb += 2) {
-            fill(s1, kb + 1);
-            use(s0);
-            fill(s0, kb + 2);
-            use(s1);
-        }
-        if (kb + 1 < KB) {
-            fill(s1, kb + 1);
-            use(s0);
-            use(s1);
-        } else {
-            use(s0);
-        }
-        write_tile<QUANT, 1, SWIGLU, BM>(p, acc, at, 0, wave, lane, wave_max);
-        __syncthreads();  // wave_max is rewritten by the next tile
-    }
-}
-
-// ---------------------------------------------------------------------------
 // Large row groups: BM rows x 256 channels per block of 8 waves.
 //
 // Rows, weights and scales of one 128-channel block form a stage, which loads
@@ -407,11 +280,6 @@ __global__ __launch_bounds__(kGemmThreads) void expert_gemm_stream(ExpertGemmArg
 // are persistent: the first stages of a block's next tile load while it
 // writes its last one's results.
 // ---------------------------------------------------------------------------
-
-constexpr int kTileThreads = 512;
-constexpr int kTileWaves = kTileThreads / kWave;
-constexpr int kMGroup = 8;   // row tiles that walk the channel tiles together
-constexpr int kWaveRows = 2, kWaveCols = 4;  // waves over the tile's rows and channels
 
 // Four of an operand's eight registers.
 __device__ __forceinline__ dev::u32x4 half(const dev::i32x8 &v, int at)
@@ -695,12 +563,15 @@ __device__ __forceinline__ void run_tile(const ExpertGemmArgs &p, const TileAt &
     // (1.15e-5 rms of them): every third block goes through bf16 operands, which
     // leaves 9.3e-6 and costs 20% (gate and up products of 32,768 skewed rows, 64
     // experts, 7168 -> 2 x 2048: 1.31 -> 1.56 ms; all blocks: 2e-7, 2.06 ms).
-    // Outputs in bf16 or with power-of-two scales do not show it.
+    // Outputs in bf16 or with power-of-two scales do not show it.  With one row
+    // fragment per wave the weights' bytes bound the step and all blocks go that
+    // way (2048 rows, 256 experts: 1211 -> 1235 us).
     constexpr bool kMixed = QUANT == MOE_QUANT_FP8_F32 && SWIGLU;
     static_assert(!kMixed || NS == 3, "one block of three");
     const std::true_type first;
-    const std::false_type fast, later;
+    const std::false_type later;
     const std::bool_constant<kMixed> mixed;
+    const std::bool_constant<kMixed && MT == 1> fast;
     step(first, mixed, st0, NS == 3 ? st2 : st1, 0);
     if constexpr (NS == 3) {
         if (KB > 1) {
@@ -734,7 +605,6 @@ __device__ __forceinline__ void run_tile(const ExpertGemmArgs &p, const TileAt &
 template <int QUANT, bool SWIGLU, int BM, int NS>
 __global__ __launch_bounds__(kTileThreads) void expert_gemm_tiles(ExpertGemmArgs p, int32_t n_tiles)
 {
-    constexpr int kGroup = 4;  // a whole table of the experts would not fit
     __shared__ int32_t tile_start[kMaxExperts / kGroup + 1];
     __shared__ int32_t red[kTileWaves];
     // separate variables: the compiler then knows which reads follow which loads
@@ -745,7 +615,7 @@ __global__ __launch_bounds__(kTileThreads) void expert_gemm_tiles(ExpertGemmArgs
     __shared__ float wave_max[SWIGLU && QUANT != MOE_QUANT_MXFP8 ? kWaveCols : 1][BM];
     const int lane = threadIdx.x & (kWave - 1);
     const int wave = scalar(threadIdx.x / kWave);
-    scan_tiles<BM, kTileThreads, kGroup>(p, tile_start, red);
+    scan_tiles<BM>(p, tile_start, red);
     const int64_t n_work = (int64_t)scalar(tile_start[(p.E + kGroup - 1) / kGroup]) * n_tiles;
     // workgroups go to the 8 XCDs in turn: each XCD takes a contiguous run of
     // the work, so that the tiles of one expert share its L2
@@ -758,7 +628,7 @@ __global__ __launch_bounds__(kTileThreads) void expert_gemm_tiles(ExpertGemmArgs
     const auto locate = [&](int64_t idx) {
         const int64_t work = base + idx;
         TileAt at;
-        const ExpertAt ex = find_expert<BM, kGroup>(p, tile_start, scalar((int32_t)(work / n_tiles)));
+        const ExpertAt ex = find_expert<BM>(p, tile_start, scalar((int32_t)(work / n_tiles)));
         const int32_t e_tiles = (ex.rows + BM - 1) / BM;
         const int64_t local = work - (int64_t)ex.start * n_tiles;
         const int32_t grp = (int32_t)(local / ((int64_t)kMGroup * n_tiles));
@@ -797,20 +667,6 @@ __global__ __launch_bounds__(kTileThreads) void expert_gemm_tiles(ExpertGemmArgs
     }
 }
 
-template <int QUANT, bool SWIGLU>
-hipError_t launch_stream(const ExpertGemmArgs &p, hipStream_t stream)
-{
-    const int32_t n_tiles = SWIGLU ? p.n / 256 : (p.n + kTileN - 1) / kTileN;
-    // a segment's last tile is partial: at most one more tile per expert that has rows
-    const int64_t parts = p.max_rows < p.E ? p.max_rows : p.E;
-    const int64_t tiles = (p.max_rows / 16 + parts) * n_tiles;
-    const int64_t cap = (int64_t)1 << 30;
-    const int64_t grid = tiles < 1 ? 1 : tiles > cap ? cap : tiles;
-    hipLaunchKernelGGL((expert_gemm_stream<QUANT, SWIGLU>), dim3((uint32_t)grid), dim3(kGemmThreads), 0, stream, p,
-                       n_tiles);
-    return hipGetLastError();
-}
-
 template <int QUANT, bool SWIGLU, int BM, int NS>
 hipError_t launch_tiles(const ExpertGemmArgs &p, hipStream_t stream)
 {
@@ -829,8 +685,6 @@ template <int QUANT, bool SWIGLU>
 hipError_t launch_rows(const ExpertGemmArgs &p, hipStream_t stream)
 {
     const int64_t per_expert = p.max_rows / p.E;
-    if (per_expert <= 16)
-        return launch_stream<QUANT, SWIGLU>(p, stream);
     if constexpr (!SWIGLU) {
         const int64_t parts = p.max_rows < p.E ? p.max_rows : p.E;
         const int64_t tiles = (p.max_rows / 256 + parts) * ((p.n + kTileN - 1) / kTileN);
