@@ -137,24 +137,12 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer(const void *p, uint32_t
                                              0x00020000);
 }
 
-// Store number `count - 1` and those before it without effect: past the end.
-template <int COUNT>
-__device__ __forceinline__ void store_nothing(__amdgpu_buffer_rsrc_t out)
-{
-#pragma unroll
-    for (int i = 0; i < COUNT; ++i)
-        __builtin_amdgcn_raw_buffer_store_b128(dev::u32x4{0, 0, 0, 0}, out, 0x80000000u, 0, 0);
-}
-
 // Waits for this wave's LDS accesses, then for the block's other waves, and
 // leaves memory accesses on their way.
 __device__ __forceinline__ void meet()
 {
     asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
 }
-
-// Stores that a wave always issues for MT row fragments (write_tile).
-constexpr int kStores(int mt) { return 2 * mt; }
 
 // Writes a wave's results: rows 16 MT wr + 16 i + (lane % 16), channels n0[f] + 4
 // (lane / 16) + j.  bf16 outputs, or (SWIGLU; fragments f < 2 hold the gate,
@@ -164,15 +152,14 @@ template <int QUANT, int MT, bool SWIGLU, int BM>
 __device__ __forceinline__ void write_tile(const ExpertGemmArgs &p, dev::f32x4 (&acc)[kNF][MT], const TileAt &at,
                                            int wr, int wc, int lane, float (*wave_max)[BM])
 {
-    constexpr int kMaxMT = BM / 32;
     const int r = lane & 15, g = lane >> 4;
     if constexpr (!SWIGLU) {
         // Two fragments' results change places between odd and even rows of 16
         // lanes: a lane then has 8 adjacent channels of its row, and 4 lanes half of
         // the row's 64.  The other half comes from the lane 8 further, for the
         // half that one needs: a store then covers whole cache lines, 128 bytes of
-        // each of 8 rows.  Rows and channels past the end go past the buffer's:
-        // every wave issues the same number of stores.  They are marked as streamed (non-temporal), which leaves L2 to the weights (8192
+        // each of 8 rows.  Rows and channels past the end go past the buffer's,
+        // which drops them.  The stores are marked as streamed (non-temporal), which leaves L2 to the weights (8192
         // dense rows, 7168 -> 8192, UE8M0: 424 -> 382 us).
         constexpr int kStreamed = 2;
         const __amdgpu_buffer_rsrc_t out = buffer(p.y + at.row0 * p.n, (uint32_t)at.valid * (uint32_t)p.n * 2);
@@ -204,7 +191,6 @@ __device__ __forceinline__ void write_tile(const ExpertGemmArgs &p, dev::f32x4 (
                 __builtin_amdgcn_raw_buffer_store_b128(v[h], out, off, 0, kStreamed);
             }
         }
-        store_nothing<kStores(kMaxMT) - kStores(MT)>(out);
     } else {
         const int32_t inter = p.n / 2;
         const __amdgpu_buffer_rsrc_t out = buffer(p.h + at.row0 * inter, (uint32_t)at.valid * (uint32_t)inter);
@@ -265,7 +251,6 @@ __device__ __forceinline__ void write_tile(const ExpertGemmArgs &p, dev::f32x4 (
                             __builtin_amdgcn_raw_buffer_store_b8((uint8_t)0, scales, soff, b, 0);
             }
         }
-        store_nothing<kStores(kMaxMT) - kStores(MT)>(out);
     }
 }
 
@@ -298,8 +283,11 @@ __device__ __forceinline__ void load_lds(__amdgpu_buffer_rsrc_t b, uint8_t *dst,
         __builtin_amdgcn_raw_ptr_buffer_load_lds(b, to, 4, voff, soff, 0, 0);
 }
 
-// Waits until at most `vm` of this wave's memory loads are outstanding and all
-// of its LDS reads are done, then for the block's other waves.
+// Waits until at most VM of this wave's memory accesses are outstanding and all
+// of its LDS reads are done, then for the block's other waves.  VM counts the
+// loads that were issued after those waited for, and loads only: stores issued
+// after loads into LDS may complete before them (a count that took the stores of
+// the tile before to be behind this tile's loads gave stages that were not there).
 template <int VM>
 __device__ __forceinline__ void wait_and_meet()
 {
@@ -543,7 +531,8 @@ __device__ __forceinline__ void run_tile(const ExpertGemmArgs &p, const TileAt &
 {
     TileLoads<QUANT, SWIGLU, BM> loads;
     loads.set(p, at, wave, lane);
-    constexpr int kAhead = Stage<BM>::kLoads * (NS - 2);
+    // the load of scales, first of its step and mostly without effect, is not counted
+    constexpr int kAhead = (Stage<BM>::kLoads - 1) * (NS - 2);
     const int wr = wave / kWaveCols, wc = wave % kWaveCols;
     const int KB = loads.KB;
     dev::f32x4 acc[kNF][MT];
@@ -552,10 +541,8 @@ __device__ __forceinline__ void run_tile(const ExpertGemmArgs &p, const TileAt &
 #pragma unroll
         for (int i = 0; i < MT; ++i)
             acc[f][i] = dev::f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-    // FIRST: the stores of the tile before may still be on their way, behind the
-    // loads of this tile's first NS - 1 stages
-    const auto step = [&](auto first, auto exact, uint8_t *cur, uint8_t *free, int kb) {
-        wait_and_meet<kAhead + (decltype(first)::value ? kStores(BM / 32) : 0)>();
+    const auto step = [&](auto exact, uint8_t *cur, uint8_t *free, int kb) {
+        wait_and_meet<kAhead>();
         multiply_stage<QUANT, SWIGLU, BM, MT, decltype(exact)::value>(acc, cur, wr, wc, lane, loads, free,
                                                                       kb + NS - 1, chunks, kb);
     };
@@ -568,33 +555,33 @@ __device__ __forceinline__ void run_tile(const ExpertGemmArgs &p, const TileAt &
     // way (2048 rows, 256 experts: 1211 -> 1235 us).
     constexpr bool kMixed = QUANT == MOE_QUANT_FP8_F32 && SWIGLU;
     static_assert(!kMixed || NS == 3, "one block of three");
-    const std::true_type first;
-    const std::false_type later;
     const std::bool_constant<kMixed> mixed;
     const std::bool_constant<kMixed && MT == 1> fast;
-    step(first, mixed, st0, NS == 3 ? st2 : st1, 0);
+    // The first steps stand before the loop: there the compiler's own waits allow
+    // for the stores of the tile before, in the loop they would hold up each turn.
+    step(mixed, st0, NS == 3 ? st2 : st1, 0);
     if constexpr (NS == 3) {
         if (KB > 1) {
-            step(first, fast, st1, st0, 1);
+            step(fast, st1, st0, 1);
             int kb = 2;
             for (; kb + 3 <= KB; kb += 3) {
-                step(later, fast, st2, st1, kb);
-                step(later, mixed, st0, st2, kb + 1);
-                step(later, fast, st1, st0, kb + 2);
+                step(fast, st2, st1, kb);
+                step(mixed, st0, st2, kb + 1);
+                step(fast, st1, st0, kb + 2);
             }
             if (kb < KB)
-                step(later, fast, st2, st1, kb);
+                step(fast, st2, st1, kb);
             if (kb + 1 < KB)
-                step(later, mixed, st0, st2, kb + 1);
+                step(mixed, st0, st2, kb + 1);
         }
     } else {
         int kb = 1;
         for (; kb + 2 <= KB; kb += 2) {
-            step(later, fast, st1, st0, kb);
-            step(later, fast, st0, st1, kb + 1);
+            step(fast, st1, st0, kb);
+            step(fast, st0, st1, kb + 1);
         }
         if (kb < KB)
-            step(later, fast, st1, st0, kb);
+            step(fast, st1, st0, kb);
     }
     wait_and_meet<0>();
     if (more)
@@ -646,8 +633,6 @@ __global__ __launch_bounds__(kTileThreads) void expert_gemm_tiles(ExpertGemmArgs
         return;
     TileAt next = locate(idx);
     start_tile<QUANT, SWIGLU, BM, NS>(p, next, st0, st1, chunks, wave, lane);
-    // as many as behind the loads of every later tile (see step)
-    store_nothing<kStores(BM / 32)>(buffer(p.a, 0));
     for (;;) {
         const TileAt at = next.scalars();
         idx += gridDim.x >> 3;

@@ -281,6 +281,39 @@ def test_products_read_weights_past_4_gib():
         assert float((y.to(D) - want).norm() / want.norm()) <= 2.0 ** -8 + 2.0 ** -15
 
 
+@pytest.mark.parametrize("quant", FORMATS)
+def test_products_do_not_depend_on_when_loads_arrive(quant):
+    """Blocks that go from tile to tile, each a few rows of another expert, with weights and
+    rows from memory (a buffer larger than the caches is written between): every run gives
+    the same bits, and the sums of the formulas."""
+    _say(f"products of many small tiles, caches cold, quant {quant}")
+    case = dict(T=96, E=64, K=6, k=1024)
+    rows = Rows(5, quant=quant, **case)
+    n, inter = 4096, 2048
+    w, ws = R.make_weights(_gen(6), 64, n, 1024, quant, "cuda")
+    cold = torch.empty(1 << 29, dtype=torch.uint8, device="cuda")
+    first = None
+    for i in range(8):
+        y = _filled((rows.rows, n), torch.bfloat16)
+        h = _filled((rows.rows, inter), torch.uint8)
+        hs = _scales(rows.rows, inter, quant)
+        cold.fill_(i)
+        M.moe_expert_gemm(rows.cfg, 96, n, 1024, rows.a, rows.s, w, ws, rows.handle, y)
+        cold.fill_(i)
+        M.moe_expert_gemm_swiglu(rows.cfg, 96, inter, rows.a, rows.s, w, ws, rows.handle, h, hs)
+        torch.cuda.synchronize()
+        got = [y[rows.used].view(torch.int16), h[rows.used], hs[rows.used].view(torch.int32)]
+        if first is None:
+            first = got
+        for a, b in zip(first, got):
+            assert torch.equal(a, b), i
+    for e in (0, 21, 42, 63):
+        o, m = rows.off[e], rows.count[e]
+        a = R.dequantize(rows.a[o:o + m], rows.s[o:o + m], quant)
+        want, bound = R.product(a, R.weight_values(w[e:e + 1], ws[e:e + 1], quant)[0])
+        R.assert_bf16(y[o:o + m], want, bound, f"expert {e}")
+
+
 def test_products_without_rows():
     _say("no token, and tokens that route nowhere")
     cfg = _cfg(8, 256, 4, 2, M.QUANT_FP8_F32, align=128)
