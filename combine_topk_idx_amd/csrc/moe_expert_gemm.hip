@@ -612,14 +612,12 @@ __global__ __launch_bounds__(kTileThreads) void expert_gemm_tiles(ExpertGemmArgs
 
     // tiles of an expert: groups of kMGroup row tiles; inside a group the row
     // tiles of one channel tile are adjacent (they share its weights)
-    const auto locate = [&](int64_t idx) {
-        const int64_t work = base + idx;
+    const auto locate = [&](int32_t m, int32_t rem) {  // number m * n_tiles + rem
         TileAt at;
-        const ExpertAt ex = find_expert<BM>(p, tile_start, scalar((int32_t)(work / n_tiles)));
+        const ExpertAt ex = find_expert<BM>(p, tile_start, m);
         const int32_t e_tiles = (ex.rows + BM - 1) / BM;
-        const int64_t local = work - (int64_t)ex.start * n_tiles;
-        const int32_t grp = (int32_t)(local / ((int64_t)kMGroup * n_tiles));
-        const int32_t in_grp = (int32_t)(local - (int64_t)grp * kMGroup * n_tiles);
+        const int32_t grp = (m - ex.start) / kMGroup;
+        const int32_t in_grp = (m - ex.start) % kMGroup * n_tiles + rem;
         const int32_t grp_rows = min(kMGroup, e_tiles - grp * kMGroup);
         at.e = scalar(ex.e);
         at.nt = scalar(in_grp / grp_rows);
@@ -631,14 +629,23 @@ __global__ __launch_bounds__(kTileThreads) void expert_gemm_tiles(ExpertGemmArgs
     int64_t idx = blockIdx.x >> 3;
     if (idx >= end)
         return;
-    TileAt next = locate(idx);
+    int32_t m = scalar((int32_t)((base + idx) / n_tiles));
+    int32_t rem = scalar((int32_t)((base + idx) - (int64_t)m * n_tiles));
+    const int32_t m_step = scalar((gridDim.x >> 3) / n_tiles), rem_step = (gridDim.x >> 3) - m_step * n_tiles;
+    TileAt next = locate(m, rem);
     start_tile<QUANT, SWIGLU, BM, NS>(p, next, st0, st1, chunks, wave, lane);
     for (;;) {
         const TileAt at = next.scalars();
         idx += gridDim.x >> 3;
         const bool more = idx < end;
+        m += m_step;
+        rem += rem_step;
+        if (rem >= n_tiles) {
+            rem -= n_tiles;
+            ++m;
+        }
         if (more)
-            next = locate(idx);
+            next = locate(m, rem);
         // a tile that is not full takes the code for its size
         constexpr int MT = BM / 16 / kWaveRows, M2 = (MT + 1) / 2, M1 = (MT + 3) / 4;
         if (at.valid > M2 * 32)
