@@ -6,10 +6,20 @@
 // One v_mfma_f32_16x16x128_f8f6f4 covers 16 output channels x 16 rows x one
 // 128-channel block.  The weights are its first operand, so a lane's four
 // results belong to one row and four adjacent output channels: the fp32 scale
-// of a block is one product per lane and the outputs leave in 8-byte pieces.
-// fp32 scales are applied to each block's result as it is added to the running
-// sum; power-of-two scales go into the matrix instruction (one byte per 32
-// channels of a lane's row) and the sum stays in its accumulator.
+// of a block is one product per lane, and lanes that trade results make whole
+// cache lines of a row.  fp32 scales are applied to each block's result as it is
+// added to the running sum; power-of-two scales go into the matrix instruction
+// (one byte per 32 channels of a lane's row) and the sum stays in its accumulator.
+//
+// Bounds and measurements (one MI355X; times of calls in a row):
+//   few rows per expert: the weights' bytes.  128 experts x 8 rows, 768 -> 2048:
+//   45 us; 256 experts x 8 rows, 7168 -> 2 x 2048, SwiGLU: 1.23 ms, 6.1 TB/s;
+//   many rows: the matrix cores and LDS.  8192 dense rows, 7168 -> 8192, UE8M0:
+//   383 us, 2510 TFLOP/s (a library's product of 8192^3 with one scale: 2718);
+//   in between: the start and end of a tile (a block's results leave while nothing
+//   multiplies), 65,536 rows of 256 experts, 2048 -> 7168: 1.35 ms, 1430 TFLOP/s.
+// Weights loaded to registers instead of LDS took twice as long (each of the two
+// wave rows reads them), blocks of 320 rows and K walks that start apart the same.
 #include <type_traits>
 
 #include "moe_mma.h"
@@ -255,15 +265,15 @@ __device__ __forceinline__ void write_tile(const ExpertGemmArgs &p, dev::f32x4 (
 }
 
 // ---------------------------------------------------------------------------
-// Large row groups: BM rows x 256 channels per block of 8 waves.
+// BM rows x 256 channels per block of 8 waves.
 //
-// Rows, weights and scales of one 128-channel block form a stage, which loads
-// straight from memory into LDS (no registers in between); NS stages are in
-// turn, so NS - 1 blocks are in flight while one is multiplied.  A wave waits
-// for its own loads of a stage, a barrier makes the others' visible, and the
-// stage that was multiplied before the barrier takes the next block.  Blocks
-// are persistent: the first stages of a block's next tile load while it
-// writes its last one's results.
+// Rows and weights of one 128-channel block form a stage, which loads straight
+// from memory into LDS (no registers in between); NS stages are in turn, so
+// NS - 1 blocks are in flight while one is multiplied.  A wave waits for its
+// own loads of a stage, a barrier makes the others' visible, and the stage that
+// was multiplied before the barrier takes the next block.  Blocks are
+// persistent, one per compute unit: the first stages of a block's next tile
+// load while it writes its last one's results.
 // ---------------------------------------------------------------------------
 
 // Four of an operand's eight registers.
@@ -676,6 +686,11 @@ hipError_t launch_tiles(const ExpertGemmArgs &p, hipStream_t stream)
 template <int QUANT, bool SWIGLU>
 hipError_t launch_rows(const ExpertGemmArgs &p, hipStream_t stream)
 {
+    // 256-row tiles read the weights half as often, with one stage less in flight
+    // and larger remainders: plain product, 2048 -> 7168, 64 experts, UE8M0, 128 /
+    // 256 rows: 256 rows per expert 376 / 397 us, 512: 630 / 616, 1024: 1183 / 1068.
+    // For SwiGLU (7168 -> 2 x 2048) 512: 1099 / 1201, 768: 1536 / 1654, 1024: 1996 /
+    // 1977, and the registers spill.  Fewer tiles than compute units: 128 rows.
     const int64_t per_expert = p.max_rows / p.E;
     if constexpr (!SWIGLU) {
         const int64_t parts = p.max_rows < p.E ? p.max_rows : p.E;

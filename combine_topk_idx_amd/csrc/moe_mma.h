@@ -41,6 +41,7 @@ __device__ __forceinline__ void to_bf16(const u32x4 &v, float scale, bf16x8 &lo,
 // and at 64 + 16 g (hi) -- as four bf16 operands of v_mfma_f32_16x16x32_bf16,
 // times the block's scale where that is a power of two (`s`: as it is stored; the
 // word of four bytes for MXFP8, whose blocks g / 2 and 2 + g / 2 the lane has).
+// Byte 0, 2^-127, is taken as 0.
 template <int QUANT>
 __device__ __forceinline__ void block_to_bf16(const u32x4 &lo, const u32x4 &hi, uint32_t s, int g, bf16x8 v[4])
 {
