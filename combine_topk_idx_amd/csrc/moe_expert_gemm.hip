@@ -528,8 +528,10 @@ __device__ __forceinline__ void start_tile(const ExpertGemmArgs &p, const TileAt
     TileLoads<QUANT, SWIGLU, BM> loads;
     loads.set(p, at, wave, lane);
     loads.template issue<0, Stage<BM>::kLoads>(st0, 0, chunks, -4);
+    __builtin_amdgcn_sched_barrier(0);  // in this order: the waits count
     if constexpr (NS == 3)
         loads.template issue<0, Stage<BM>::kLoads>(st1, 1, chunks, -3);
+    __builtin_amdgcn_sched_barrier(0);
 }
 
 // Multiplies a tile whose first NS - 1 stages are in flight, then starts the
