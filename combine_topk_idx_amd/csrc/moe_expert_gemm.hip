@@ -12,6 +12,7 @@
 // (one byte per 32 channels of a lane's row) and the sum stays in its accumulator.
 //
 // Bounds and measurements (one MI355X; times of calls in a row):
+//   a few rows in all: latency (expert_gemm_strips).  One row, 7168 -> 7168: 15 us;
 //   few rows per expert: the weights' bytes.  128 experts x 8 rows, 768 -> 2048:
 //   45 us; 256 experts x 8 rows, 7168 -> 2 x 2048, SwiGLU: 1.23 ms, 6.1 TB/s;
 //   many rows: the matrix cores and LDS.  8192 dense rows, 7168 -> 8192, UE8M0:
@@ -671,12 +672,131 @@ __global__ __launch_bounds__(kTileThreads) void expert_gemm_tiles(ExpertGemmArgs
     }
 }
 
+// ---------------------------------------------------------------------------
+// Few rows and too few tiles for the chip: 16 rows x 16 channels per block, whose
+// waves share the blocks of 128 input channels and add up in LDS, in order.
+//
+// Bound by latency: the tiles above would leave most compute units idle, with
+// one step's round trip to memory after the other.
+// ---------------------------------------------------------------------------
+
+template <int QUANT>
+__global__ __launch_bounds__(kTileThreads) void expert_gemm_strips(ExpertGemmArgs p, int32_t strips)
+{
+    __shared__ int32_t tile_start[kMaxExperts / kGroup + 1];
+    __shared__ int32_t red[kTileWaves];
+    __shared__ dev::f32x4 part[kTileWaves][kWave];
+    const int lane = threadIdx.x & (kWave - 1);
+    const int wave = scalar(threadIdx.x / kWave);
+    const int r = lane & 15, g = lane >> 4;
+    const int KB = p.k / kQuantGroup;
+    const int KW = (KB + 3) / 4;
+    const int NBn = (p.n + kQuantGroup - 1) / kQuantGroup;
+    scan_tiles<16>(p, tile_start, red);
+    const int64_t n_work = (int64_t)scalar(tile_start[(p.E + kGroup - 1) / kGroup]) * strips;
+
+    for (int64_t work = blockIdx.x; work < n_work; work += gridDim.x) {
+        const int32_t m = scalar((int32_t)(work / strips));
+        const int32_t c0 = scalar((int32_t)(work - (int64_t)m * strips)) * 16;
+        const ExpertAt ex = find_expert<16>(p, tile_start, m);
+        const int32_t first = (m - ex.start) * 16, valid = min(16, ex.rows - first);
+        const int64_t row0 = (int64_t)(p.expert_offset != nullptr ? word_of(p.expert_offset, ex.e) : 0) + first;
+        // rows past the end: the last one, channels past the end: the last one
+        const int64_t arow = row0 + min(r, valid - 1);
+        const int32_t c = min(c0 + r, p.n - 1);
+        const int64_t wrow = (int64_t)ex.e * p.n + c;
+        const int64_t srow = QUANT == MOE_QUANT_MXFP8 ? wrow : (int64_t)ex.e * NBn + c0 / kQuantGroup;
+        struct Block {
+            dev::u32x4 w[2], x[2];
+            uint32_t sw, sx;  // scales as they are stored
+        };
+        const auto fill = [&](Block &b, int kb) {
+            const uint8_t *w = p.w + wrow * p.k + (int64_t)kb * kQuantGroup + 16 * g;
+            const uint8_t *x = p.a + arow * p.k + (int64_t)kb * kQuantGroup + 16 * g;
+            b.w[0] = *reinterpret_cast<const dev::u32x4 *>(w);
+            b.w[1] = *reinterpret_cast<const dev::u32x4 *>(w + 64);
+            b.x[0] = *reinterpret_cast<const dev::u32x4 *>(x);
+            b.x[1] = *reinterpret_cast<const dev::u32x4 *>(x + 64);
+            if constexpr (QUANT == MOE_QUANT_FP8_UE8M0) {
+                b.sw = static_cast<const uint8_t *>(p.w_scale)[srow * KW * 4 + kb];
+                b.sx = static_cast<const uint8_t *>(p.a_scale)[arow * KW * 4 + kb];
+            } else {
+                b.sw = static_cast<const uint32_t *>(p.w_scale)[srow * KB + kb];
+                b.sx = static_cast<const uint32_t *>(p.a_scale)[arow * KB + kb];
+            }
+            __builtin_amdgcn_sched_barrier(0);
+        };
+        dev::f32x4 acc = {0.0f, 0.0f, 0.0f, 0.0f};
+        const auto use = [&](const Block &b) {
+            const dev::f32x4 z = {0.0f, 0.0f, 0.0f, 0.0f};
+            if constexpr (QUANT == MOE_QUANT_FP8_F32) {
+                const dev::f32x4 d = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
+                    join(b.w[0], b.w[1]), join(b.x[0], b.x[1]), z, 0, 0, 0, 0, 0, 0);
+                const float s = __uint_as_float(b.sx) * __uint_as_float(b.sw);
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    acc[j] = __builtin_fmaf(d[j], s, acc[j]);
+            } else {
+                const int shift = QUANT == MOE_QUANT_MXFP8 ? 8 * g : 0;
+                acc = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
+                    join(b.w[0], b.w[1]), join(b.x[0], b.x[1]), acc, 0, 0, 0, (int)(b.sw >> shift), 0,
+                    (int)(b.sx >> shift));
+            }
+            __builtin_amdgcn_sched_barrier(0);
+        };
+        constexpr int S = kTileWaves;
+        if (wave < KB) {
+            // four blocks in flight; past the last one, the last one again
+            const int count = (KB - wave + S - 1) / S, last = wave + (count - 1) * S;
+            Block b0, b1, b2, b3;
+            fill(b0, wave);
+            fill(b1, min(wave + S, last));
+            fill(b2, min(wave + 2 * S, last));
+            for (int i = 0; i < count; i += 4) {
+                const int kb = wave + i * S;
+                fill(b3, min(kb + 3 * S, last));
+                use(b0);
+                if (i + 1 >= count)
+                    break;
+                fill(b0, min(kb + 4 * S, last));
+                use(b1);
+                if (i + 2 >= count)
+                    break;
+                fill(b1, min(kb + 5 * S, last));
+                use(b2);
+                if (i + 3 >= count)
+                    break;
+                fill(b2, min(kb + 6 * S, last));
+                use(b3);
+            }
+        }
+        part[wave][lane] = acc;
+        __syncthreads();
+        if (wave == 0) {
+#pragma unroll
+            for (int w = 1; w < kTileWaves; ++w)
+                acc += part[w][lane];
+            if (r < valid && c0 + 4 * g < p.n)
+                *reinterpret_cast<uint2 *>(p.y + (row0 + r) * p.n + c0 + 4 * g) =
+                    make_uint2(dev::pack_bf16(acc[0], acc[1]), dev::pack_bf16(acc[2], acc[3]));
+        }
+        __syncthreads();  // part is rewritten by the next strip
+    }
+}
+
+// Row tiles of `rows` rows that a call can have: a segment's last one is partial.
+int64_t max_tiles(const ExpertGemmArgs &p, int32_t rows)
+{
+    if (p.recv_count == nullptr)
+        return (p.max_rows + rows - 1) / rows;
+    return p.max_rows / rows + (p.max_rows < p.E ? p.max_rows : p.E);
+}
+
 template <int QUANT, bool SWIGLU, int BM, int NS>
 hipError_t launch_tiles(const ExpertGemmArgs &p, hipStream_t stream)
 {
     const int32_t n_tiles = SWIGLU ? p.n / 256 : (p.n + kTileN - 1) / kTileN;
-    const int64_t parts = p.max_rows < p.E ? p.max_rows : p.E;
-    const int64_t tiles = (p.max_rows / BM + parts) * n_tiles;
+    const int64_t tiles = max_tiles(p, BM) * n_tiles;
     // one block per compute unit (its stages fill LDS), a multiple of the 8 XCDs
     const int64_t cus = (device_cu_count() + 7) / 8 * 8;
     const int64_t grid = tiles < cus ? (tiles + 7) / 8 * 8 : cus;
@@ -688,16 +808,27 @@ hipError_t launch_tiles(const ExpertGemmArgs &p, hipStream_t stream)
 template <int QUANT, bool SWIGLU>
 hipError_t launch_rows(const ExpertGemmArgs &p, hipStream_t stream)
 {
-    // 256-row tiles read the weights half as often, with one stage less in flight
-    // and larger remainders: plain product, 2048 -> 7168, 64 experts, UE8M0, 128 /
-    // 256 rows: 256 rows per expert 376 / 397 us, 512: 630 / 616, 1024: 1183 / 1068.
-    // For SwiGLU (7168 -> 2 x 2048) 512: 1099 / 1201, 768: 1536 / 1654, 1024: 1996 /
-    // 1977, and the registers spill.  Fewer tiles than compute units: 128 rows.
-    const int64_t per_expert = p.max_rows / p.E;
     if constexpr (!SWIGLU) {
-        const int64_t parts = p.max_rows < p.E ? p.max_rows : p.E;
-        const int64_t tiles = (p.max_rows / 256 + parts) * ((p.n + kTileN - 1) / kTileN);
-        if (per_expert >= 512 && tiles >= device_cu_count())
+        const int64_t cus = device_cu_count();
+        // Strips while there are few: a block's round trips take 5 us and more, and two
+        // blocks fit a compute unit.  fp32 scales, in a graph, tiles / strips: one row,
+        // 512 -> 512 6.8 / 3.8 us, 2048 -> 2048 13.1 / 5.6, 7168 -> 7168 (448 strips) 35.6 /
+        // 15.3; 32 rows, 7168 -> 7168 (896) 36 / 47; 64 rows, 2048 -> 2048 (512) 15.2 / 13.7,
+        // MXFP8 13.4 / 15.9; 4 rows each of 16 experts, 7168 ->
+        // 512 (640) 36.5 / 19.4, of 8 experts, 2048 -> 2048 (1280) 14.6 / 20.8.
+        const int32_t strips = (p.n + 15) / 16;
+        const int64_t work = max_tiles(p, 16) * strips;
+        if (2 * work <= 5 * cus) {
+            hipLaunchKernelGGL((expert_gemm_strips<QUANT>), dim3((uint32_t)work), dim3(kTileThreads), 0, stream, p,
+                               strips);
+            return hipGetLastError();
+        }
+        // 256-row tiles read the weights half as often, with one stage less in flight
+        // and larger remainders: plain product, 2048 -> 7168, 64 experts, UE8M0, 128 /
+        // 256 rows: 256 rows per expert 376 / 397 us, 512: 630 / 616, 1024: 1183 / 1068.
+        // For SwiGLU (7168 -> 2 x 2048) 512: 1099 / 1201, 768: 1536 / 1654, 1024: 1996 /
+        // 1977, and the registers spill.  Fewer tiles than compute units: 128 rows.
+        if (p.max_rows / p.E >= 512 && max_tiles(p, 256) * ((p.n + kTileN - 1) / kTileN) >= cus)
             return launch_tiles<QUANT, SWIGLU, 256, 2>(p, stream);
     }
     return launch_tiles<QUANT, SWIGLU, 128, 3>(p, stream);

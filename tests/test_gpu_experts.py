@@ -183,6 +183,15 @@ CASES = [
     # 256-row tiles: enough of them for every compute unit
     dict(T=2309, E=1, K=1, k=384, n=8200, layout="dense"),
     dict(T=1300, E=2, K=1, k=256, n=16384, align=128),
+    # few rows, more 16-channel strips than the chip takes at once
+    dict(T=1, E=1, K=1, k=128, n=10264, layout="dense"),
+    dict(T=3, E=5, K=2, k=256, n=4104),
+    dict(T=40, E=16, K=2, k=640, n=776, layout="masked", capacity=3),
+    dict(T=100, E=64, K=4, k=256, n=520, skew=2.0, align=8),
+    dict(T=257, E=3, K=1, k=512, n=1288, layout="masked", capacity=200, skew=3.0),
+    # few strips: many rows of few channels, long rows
+    dict(T=2000, E=3, K=2, k=384, n=24, align=16),
+    dict(T=16, E=1, K=1, k=5120, n=264, layout="dense"),
 ]
 
 
