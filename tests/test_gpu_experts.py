@@ -192,6 +192,9 @@ CASES = [
     # few strips: many rows of few channels, long rows
     dict(T=2000, E=3, K=2, k=384, n=24, align=16),
     dict(T=16, E=1, K=1, k=5120, n=264, layout="dense"),
+    # many experts, most without rows, their number no multiple of the table's groups
+    dict(T=60, E=2047, K=1, k=128, n=264),
+    dict(T=60, E=2047, K=1, k=128, n=8),
 ]
 
 
@@ -378,6 +381,7 @@ LAYERS = [
     dict(T=64, E=2, K=1, H=128, inter=256),
     dict(T=3, E=4, K=2, H=8192, inter=128),             # wide outputs
     dict(T=40, E=64, K=32, H=128, inter=128),           # the largest top-k
+    dict(T=64, E=2048, K=32, H=128, inter=128),         # as many pairs as experts, most used
 ]
 
 
