@@ -61,8 +61,8 @@ __device__ __forceinline__ void block_to_bf16(const u32x4 &lo, const u32x4 &hi, 
 __device__ __forceinline__ float swiglu(float g, float u) { return g / (1.0f + expf(-g)) * u; }
 
 // The scale of a block with largest magnitude `amax`, the factor that E4M3
-// values are made with, and how the scale is stored -- the rules of the
-// dispatch (store_item in moe_device.h).
+// values are made with, and how the scale is stored -- for finite values the
+// rules of the dispatch (store_item in moe_device.h).  A maximum passes over NaN.
 template <int QUANT>
 struct BlockScale {
     float s;        // FP8_F32: values are divided by it; power-of-two formats: multiplied by it
@@ -85,7 +85,8 @@ struct BlockScale {
     __device__ __forceinline__ float apply(float v) const
     {
         const float d = QUANT == MOE_QUANT_FP8_F32 ? v / s : v * s;
-        return fminf(fmaxf(d, -448.0f), 448.0f);
+        const float in = fminf(fmaxf(d, -448.0f), 448.0f);
+        return d != d ? d : in;  // the clamp alone would make a NaN -448
     }
 };
 

@@ -22,6 +22,12 @@
  * enqueued on `stream` and capturable in a HIP graph.  Results do not depend
  * on timing: no sum's order is left to the scheduling.
  *
+ * Values that are not finite: a product with a NaN is NaN, and 8-bit rows keep
+ * it (E4M3 NaN) beside the scale of the block's other values.  A block with an
+ * infinite value has the scale +infinity and NaN in its place (FP8_F32), or
+ * the scale 2^120 and +-448 (UE8M0, MXFP8); what is small against its scale is
+ * 0.  Rows and tokens are independent: none shows in another's result.
+ *
  * Weight formats, by cfg.quant (w has `n` output channels of `k` input
  * channels per expert):
  *   FP8_F32    w E4M3 [E, n, k], w_scale fp32 [E, ceil(n/128), k/128]

@@ -1,0 +1,136 @@
+"""The expert-layer operators where they can go wrong: values that are not
+finite, channels that cancel, long sums, kernel variants that need large calls.
+
+Compared with 64-bit references (tests/expert_reference.py) or with the bytes of
+a call that must agree.  Every comparison fails on a NaN it does not ask for.
+Every test prints the case it runs before touching the GPU.
+"""
+import pytest
+import torch
+
+import combine_topk_idx_amd as M
+import expert_reference as R
+from test_gpu_experts import _cfg, _filled, _gen, _gpu, _say, _scales  # noqa: F401 (_gpu: a fixture)
+
+pytestmark = pytest.mark.gpu
+D = R.D
+FORMATS = [M.QUANT_FP8_F32, M.QUANT_FP8_UE8M0, M.QUANT_MXFP8]
+INF, NAN = float("inf"), float("nan")
+
+
+def _is_nan(q):
+    """E4M3 NaN, of either sign."""
+    return (q & 0x7F) == 0x7F
+
+
+def _bytes_equal(a, b, what):
+    assert torch.equal(a.contiguous().view(torch.uint8), b.contiguous().view(torch.uint8)), what
+
+
+# ---- values that are not finite ----------------------------------------------------------
+
+
+def _norm(x, w, quant, residual=None):
+    T, H = x.shape
+    out, q, s = _filled((T, H), torch.bfloat16), _filled((T, H), torch.uint8), _scales(T, H, quant)
+    res_out = None if residual is None else _filled((T, H), torch.bfloat16)
+    M.moe_rmsnorm(_cfg(T, H, quant=quant), T, x, residual, w, 1e-6, res_out, out, q, s)
+    torch.cuda.synchronize()
+    return out, q, s
+
+
+@pytest.mark.parametrize("quant", FORMATS)
+@pytest.mark.parametrize("bad", [NAN, INF, -INF])
+def test_rmsnorm_of_a_token_that_is_not_finite(bad, quant):
+    """NaN in a row: all of it.  An infinity: the mean of squares is infinite, so that channel is NaN and
+    the others are 0.  The other rows are as without it."""
+    _say(f"rmsnorm, one channel of one token {bad}, quant={quant}")
+    g = _gen(3)
+    x = torch.randn(5, 640, generator=g, device="cuda").bfloat16()
+    w = torch.randn(640, generator=g, device="cuda").bfloat16()
+    clean = _norm(x, w, quant)
+    x2 = x.clone()
+    x2[2, 300] = bad
+    got = _norm(x2, w, quant)
+    for a, b in zip(got, clean):
+        _bytes_equal(a[[0, 1, 3, 4]], b[[0, 1, 3, 4]], "another token")
+    out, q = got[0][2], got[1][2]
+    at = torch.zeros(640, dtype=torch.bool, device="cuda")
+    at[300] = True
+    if bad != bad:
+        at[:] = True
+    assert torch.equal(out.isnan(), at) and torch.equal(_is_nan(q), at)
+    assert not bool((q[~at] & 0x7F).any())
+
+
+@pytest.mark.parametrize("quant", FORMATS)
+def test_rmsnorm_with_a_weight_that_is_not_finite(quant):
+    """A NaN weight makes its channel NaN; scale and bytes of the others are those of a channel that is 0."""
+    _say(f"rmsnorm, one weight NaN, quant={quant}")
+    g = _gen(4)
+    x = torch.randn(7, 512, generator=g, device="cuda").bfloat16()
+    w = torch.randn(512, generator=g, device="cuda").bfloat16()
+    w[130] = 0.0
+    zero = _norm(x, w, quant)
+    w[130] = NAN
+    out, q, s = _norm(x, w, quant)
+    _bytes_equal(s, zero[2], "scales")
+    rest = torch.arange(512, device="cuda") != 130
+    _bytes_equal(q[:, rest], zero[1][:, rest], "other channels")
+    assert bool(_is_nan(q[:, 130]).all()) and bool(out[:, 130].isnan().all()) and not bool(out[:, rest].isnan().any())
+
+
+@pytest.mark.parametrize("quant", FORMATS)
+def test_rmsnorm_past_the_range_of_fp32(quant):
+    """A channel whose normed value is infinite: NaN beside an infinite fp32 scale, else the largest E4M3
+    value, with its sign, beside 2^120; the other blocks are as they were."""
+    _say(f"rmsnorm, one channel past fp32's range, quant={quant}")
+    x = torch.ones(2, 256, device="cuda").bfloat16()
+    x[:, 5] = 64.0            # 64 / sqrt((64^2 + 255) / 256) = 15.5 times the weight
+    x[1] *= -1.0
+    w = torch.ones(256, device="cuda").bfloat16()
+    clean = _norm(x, w, quant)
+    w[5] = 3.0e38
+    out, q, s = _norm(x, w, quant)
+    block = 32 if quant == M.QUANT_MXFP8 else 128
+    _bytes_equal(q[:, block:], clean[1][:, block:], "other blocks")
+    assert out[0, 5] == INF and out[1, 5] == -INF
+    if quant == M.QUANT_FP8_F32:
+        assert bool((s[:, 0] == INF).all()) and bool(_is_nan(q[:, 5]).all())
+    else:
+        assert s.view(torch.uint8)[:, 0].tolist() == [247, 247]  # 2^(247 - 127)
+        assert q[:, 5].tolist() == [0x7E, 0xFE]
+    rest = torch.arange(block, device="cuda") != 5
+    assert not bool((q[:, :block][:, rest] & 0x7F).any())
+
+
+@pytest.mark.parametrize("quant", FORMATS)
+@pytest.mark.parametrize("T", [3, 150])
+def test_products_of_a_row_with_nan(T, quant):
+    """One NaN among a row's inputs: every channel of its product, of its SwiGLU rows and of their product is
+    NaN, the other rows' bytes are as without it."""
+    _say(f"products, T={T}, one input NaN, quant={quant}")
+    k, inter = 384, 256
+    g = _gen(T)
+    a, s = R.quantize(torch.randn(T, k, generator=g, device="cuda"), quant)
+    w13, s13 = R.make_weights(g, 1, 2 * inter, k, quant, "cuda")
+    w2, s2 = R.make_weights(g, 1, k, inter, quant, "cuda")
+    cfg = _cfg(T, k, quant=quant)
+
+    def run(a):
+        y, h, hs = _filled((T, 2 * inter), torch.bfloat16), _filled((T, inter), torch.uint8), _scales(T, inter, quant)
+        z = _filled((T, k), torch.bfloat16)
+        M.moe_expert_gemm(cfg, T, 2 * inter, k, a, s, w13, s13, None, y)
+        M.moe_expert_gemm_swiglu(cfg, T, inter, a, s, w13, s13, None, h, hs)
+        M.moe_expert_gemm(cfg, T, k, inter, h, hs, w2, s2, None, z)
+        torch.cuda.synchronize()
+        return y, h, hs, z
+
+    clean = run(a)
+    bad = a.clone()
+    bad[1, 200] = 0x7F
+    got = run(bad)
+    rest = torch.arange(T, device="cuda") != 1
+    for i, (u, v) in enumerate(zip(got, clean)):
+        _bytes_equal(u[rest], v[rest], f"another row of output {i}")
+    assert bool(got[0][1].isnan().all()) and bool(_is_nan(got[1][1]).all()) and bool(got[3][1].isnan().all())
