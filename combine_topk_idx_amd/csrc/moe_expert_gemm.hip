@@ -431,17 +431,26 @@ struct TileLoads {
 // spread over the matrix instructions (all at once they would hold up the
 // wave's LDS reads until the address unit has taken them).
 //
-// EXACT: through bf16 operands.  The 8-bit instruction adds its products eight
-// at a time, aligned to the largest of the eight, and drops what lies 13 binary
-// places below that one: 1.4e-5 (rms) of a block's result, where the bf16 one
-// stays near 1e-8 at half the rate.
-template <int QUANT, bool SWIGLU, int BM, int MT, bool EXACT>
+// The 8-bit instruction adds its products eight at a time, aligned to the
+// largest of the eight, and drops what lies 13 binary places below that one:
+// 1.4e-5 (rms) of a block's result, where the bf16 instruction stays near 1e-8
+// at half the rate.  A bf16 result, or values in 8 bits beside a power of two,
+// hide that under their own rounding (2^-8, 2^-4); the fp32 scales of SwiGLU's
+// rows show it, so in that format every block goes through bf16 operands,
+// which hold E4M3 values exactly.  8-bit / bf16 there: 32,768 skewed rows, 64
+// experts, 7168 -> 2 x 2048, 1.40 / 2.21 ms, scales 1.15e-5 / 2e-7 off (rms); 2048
+// rows, 256 experts 1.21 / 1.31 ms.
+template <int QUANT, bool SWIGLU>
+constexpr bool through_bf16() { return QUANT == MOE_QUANT_FP8_F32 && SWIGLU; }
+
+template <int QUANT, bool SWIGLU, int BM, int MT>
 __device__ __forceinline__ void multiply_stage(dev::f32x4 (&acc)[kNF][MT], const uint8_t *st, int wr, int wc, int lane,
                                                const TileLoads<QUANT, SWIGLU, BM> &loads, uint8_t *free, int kb_load,
                                                uint8_t *chunks, int kb)
 {
     using C = Chunk<QUANT, BM>;
     constexpr int kLoads = Stage<BM>::kLoads;
+    constexpr bool kBf16 = through_bf16<QUANT, SWIGLU>();
     const int r = lane & 15, g = lane >> 4;
     const int rswz = (r >> 1) & 7;
     const int rlo = r * kQuantGroup + ((g ^ rswz) * 16), rhi = r * kQuantGroup + (((4 + g) ^ rswz) * 16);
@@ -450,6 +459,7 @@ __device__ __forceinline__ void multiply_stage(dev::f32x4 (&acc)[kNF][MT], const
     const uint8_t *sc = chunks + ((kb >> 2) & 1) * C::kBytes + (QUANT == MOE_QUANT_FP8_UE8M0 ? 0 : 4 * u);
     const auto scale = [&](int entry) { return *reinterpret_cast<const uint32_t *>(sc + entry * C::kWord); };
     dev::i32x8 w[kNF], x[2];
+    dev::bf16x8 wv[kBf16 ? kNF : 1][4];
     uint32_t sx[MT];
     int swb[kNF];
     float swf[2];
@@ -489,18 +499,18 @@ __device__ __forceinline__ void multiply_stage(dev::f32x4 (&acc)[kNF][MT], const
             const float s1 = SWIGLU ? __uint_as_float(sx[i]) * swf[1] : s0;
             dev::f32x4 d[kNF];
             dev::bf16x8 xv[4];
-            if constexpr (EXACT)
+            if constexpr (kBf16)
                 dev::block_to_bf16<QUANT>(half(x[i & 1], 0), half(x[i & 1], 4), 0, g, xv);
 #pragma unroll
             for (int f = 0; f < kNF; ++f) {
                 const dev::f32x4 z = {0.0f, 0.0f, 0.0f, 0.0f};
-                if constexpr (EXACT) {
-                    dev::bf16x8 wv[4];
-                    dev::block_to_bf16<QUANT>(half(w[f], 0), half(w[f], 4), 0, g, wv);
+                if constexpr (kBf16) {
+                    if constexpr (i == 0)
+                        dev::block_to_bf16<QUANT>(half(w[f], 0), half(w[f], 4), 0, g, wv[f]);
                     d[f] = z;
 #pragma unroll
                     for (int j = 0; j < 4; ++j)
-                        d[f] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wv[j], xv[j], d[f], 0, 0, 0);
+                        d[f] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wv[f][j], xv[j], d[f], 0, 0, 0);
                 } else {
                     d[f] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(w[f], x[i & 1], z, 0, 0, 0, 0, 0, 0);
                 }
@@ -557,47 +567,35 @@ __device__ __forceinline__ void run_tile(const ExpertGemmArgs &p, const TileAt &
 #pragma unroll
         for (int i = 0; i < MT; ++i)
             acc[f][i] = dev::f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-    const auto step = [&](auto exact, uint8_t *cur, uint8_t *free, int kb) {
+    const auto step = [&](uint8_t *cur, uint8_t *free, int kb) {
         wait_and_meet<kAhead>();
-        multiply_stage<QUANT, SWIGLU, BM, MT, decltype(exact)::value>(acc, cur, wr, wc, lane, loads, free,
-                                                                      kb + NS - 1, chunks, kb);
+        multiply_stage<QUANT, SWIGLU, BM, MT>(acc, cur, wr, wc, lane, loads, free, kb + NS - 1, chunks, kb);
     };
-    // The fp32 scales of SwiGLU's output would show the 8-bit instruction's error
-    // (1.15e-5 rms of them): every third block goes through bf16 operands, which
-    // leaves 9.3e-6 and costs 20% (gate and up products of 32,768 skewed rows, 64
-    // experts, 7168 -> 2 x 2048: 1.31 -> 1.56 ms; all blocks: 2e-7, 2.06 ms).
-    // Outputs in bf16 or with power-of-two scales do not show it.  With one row
-    // fragment per wave the weights' bytes bound the step and all blocks go that
-    // way (2048 rows, 256 experts: 1211 -> 1235 us).
-    constexpr bool kMixed = QUANT == MOE_QUANT_FP8_F32 && SWIGLU;
-    static_assert(!kMixed || NS == 3, "one block of three");
-    const std::bool_constant<kMixed> mixed;
-    const std::bool_constant<kMixed && MT == 1> fast;
     // The first steps stand before the loop: there the compiler's own waits allow
     // for the stores of the tile before, in the loop they would hold up each turn.
-    step(mixed, st0, NS == 3 ? st2 : st1, 0);
+    step(st0, NS == 3 ? st2 : st1, 0);
     if constexpr (NS == 3) {
         if (KB > 1) {
-            step(fast, st1, st0, 1);
+            step(st1, st0, 1);
             int kb = 2;
             for (; kb + 3 <= KB; kb += 3) {
-                step(fast, st2, st1, kb);
-                step(mixed, st0, st2, kb + 1);
-                step(fast, st1, st0, kb + 2);
+                step(st2, st1, kb);
+                step(st0, st2, kb + 1);
+                step(st1, st0, kb + 2);
             }
             if (kb < KB)
-                step(fast, st2, st1, kb);
+                step(st2, st1, kb);
             if (kb + 1 < KB)
-                step(mixed, st0, st2, kb + 1);
+                step(st0, st2, kb + 1);
         }
     } else {
         int kb = 1;
         for (; kb + 2 <= KB; kb += 2) {
-            step(fast, st1, st0, kb);
-            step(fast, st0, st1, kb + 1);
+            step(st1, st0, kb);
+            step(st0, st1, kb + 1);
         }
         if (kb < KB)
-            step(fast, st1, st0, kb);
+            step(st1, st0, kb);
     }
     wait_and_meet<0>();
     if (more)

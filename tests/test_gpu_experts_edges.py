@@ -134,3 +134,65 @@ def test_products_of_a_row_with_nan(T, quant):
     for i, (u, v) in enumerate(zip(got, clean)):
         _bytes_equal(u[rest], v[rest], f"another row of output {i}")
     assert bool(got[0][1].isnan().all()) and bool(_is_nan(got[1][1]).all()) and bool(got[3][1].isnan().all())
+
+
+# ---- sums -----------------------------------------------------------------------------------
+
+
+def _cancelling(T, blocks, n, g):
+    """E4M3 rows [T, 128 blocks] and weights [n, 128 blocks] of whole numbers, whose products and partial sums
+    are whole numbers below 2^24 (exact in fp32 in any order).  Row r has, in block r % blocks, two adjacent
+    channels whose products with every weight are 448^2 and -448^2; the rest are products of -1, 0 and 1."""
+    k = 128 * blocks
+    a = torch.randint(-1, 2, (T, k), generator=g, device="cuda").float()
+    w = torch.randint(-1, 2, (n, k), generator=g, device="cuda").float()
+    w *= (torch.rand(n, k, generator=g, device="cuda") < 0.2)
+    loud = 128 * torch.arange(blocks, device="cuda") + 40
+    a[:, loud] = 0.0
+    a[:, loud + 1] = 0.0
+    w[:, loud] = 448.0
+    w[:, loud + 1] = -448.0
+    r = torch.arange(T, device="cuda")
+    a[r, loud[r % blocks]] = 448.0
+    a[r, loud[r % blocks] + 1] = 448.0
+    return a, w
+
+
+@pytest.mark.parametrize("T", [5, 33, 100, 300])
+def test_swiglu_rows_with_fp32_scales_come_of_fp32_sums(T):
+    """Loud channels that cancel, in each of seven blocks: what is left of the sum is what is beside them."""
+    _say(f"expert_gemm_swiglu of cancelling channels, T={T}")
+    quant, inter, blocks = M.QUANT_FP8_F32, 256, 7
+    g = _gen(T)
+    a, w = _cancelling(T, blocks, 2 * inter, g)
+    y = a.double() @ w.double().T
+    assert float(y.abs().max()) < 60.0 and float(y.abs().mean()) > 3.0
+    to8 = lambda v: v.to(R.F8).view(torch.uint8)  # noqa: E731
+    s = torch.ones(T, blocks, device="cuda")
+    ws = torch.ones(1, 2 * inter // 128, blocks, device="cuda")
+    h, hs = _filled((T, inter), torch.uint8), _scales(T, inter, quant)
+    M.moe_expert_gemm_swiglu(_cfg(T, 128 * blocks, quant=quant), T, inter, to8(a), s, to8(w)[None], ws, None, h, hs)
+    torch.cuda.synchronize()
+    gate, up = y[:, :inter], y[:, inter:]
+    want = R.silu(gate) * up
+    # exact sums; the function itself in fp32 (an exponential of argument g: |g| ulps)
+    R.assert_rows(h, hs, want, want.abs() * (8 + gate.abs()) * 2.0 ** -24, quant, "h")
+
+
+@pytest.mark.parametrize("quant", FORMATS)
+def test_a_swiglu_row_does_not_depend_on_the_rows_beside_it(quant):
+    """The same row in calls of every size: the same bytes."""
+    _say(f"expert_gemm_swiglu of 1 .. 300 rows, quant={quant}")
+    k, inter, T = 1152, 256, 300
+    g = _gen(9)
+    a, s = R.quantize(torch.randn(T, k, generator=g, device="cuda"), quant)
+    w, ws = R.make_weights(g, 1, 2 * inter, k, quant, "cuda")
+    full = None
+    for t in (300, 129, 128, 127, 97, 96, 65, 64, 33, 32, 17, 1):
+        h, hs = _filled((t, inter), torch.uint8), _scales(t, inter, quant)
+        M.moe_expert_gemm_swiglu(_cfg(t, k, quant=quant), t, inter, a[:t], s[:t], w, ws, None, h, hs)
+        torch.cuda.synchronize()
+        if full is None:
+            full = h, hs
+        _bytes_equal(h, full[0][:t], f"{t} rows")
+        _bytes_equal(hs, full[1][:t], f"scales of {t} rows")
