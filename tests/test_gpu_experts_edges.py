@@ -196,3 +196,30 @@ def test_a_swiglu_row_does_not_depend_on_the_rows_beside_it(quant):
             full = h, hs
         _bytes_equal(h, full[0][:t], f"{t} rows")
         _bytes_equal(hs, full[1][:t], f"scales of {t} rows")
+
+
+@pytest.mark.parametrize("quant", FORMATS)
+@pytest.mark.parametrize("T,n", [(5, 264), (130, 520), (2400, 8200)])
+def test_products_of_cancelling_channels_stay_within_the_stated_bound(T, n, quant):
+    """16-row strips, 128-row and 256-row tiles: each group of eight adjacent channels is off by at most
+    7 * 2^-13 of its largest product, and by nothing where that one is small."""
+    _say(f"expert_gemm of cancelling channels, T={T}, n={n}, quant={quant}")
+    blocks = 7
+    g = _gen(T + n)
+    a, w = _cancelling(T, blocks, n, g)
+    a[::2] = torch.where(a[::2].abs() > 1, torch.zeros_like(a[::2]), a[::2])  # rows without a loud channel
+    k = 128 * blocks
+    to8 = lambda v: v.to(R.F8).view(torch.uint8)  # noqa: E731
+    words = {M.QUANT_FP8_F32: lambda r: torch.ones(r, blocks, device="cuda"),
+             M.QUANT_FP8_UE8M0: lambda r: torch.full((r, 8), 127, dtype=torch.uint8, device="cuda").view(torch.int32),
+             M.QUANT_MXFP8: lambda r: torch.full((r, k // 32), 127, dtype=torch.uint8, device="cuda")}[quant]
+    y = _filled((T, n), torch.bfloat16)
+    M.moe_expert_gemm(_cfg(T, k, quant=quant), T, n, k, to8(a), words(T),
+                      to8(w)[None], words(n if quant == M.QUANT_MXFP8 else -(-n // 128))[None], None, y)
+    torch.cuda.synchronize()
+    want = a.double() @ w.double().T
+    err = (y.double() - want).abs()
+    half_step = want.abs() * 2.0 ** -8
+    assert bool((err[::2] <= half_step[::2]).all()), "rows without loud channels"
+    # every weight is loud (448) at the one loud channel of the other rows
+    assert bool((err <= half_step + (1 + 2.0 ** -8) * 7 * 2.0 ** -13 * 448.0 ** 2).all())
