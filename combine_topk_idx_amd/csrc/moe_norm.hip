@@ -56,7 +56,8 @@ __global__ __launch_bounds__(THREADS *ROWS) void rmsnorm_kernel(NormArgs a)
             v[i] = rv[i] = wv[i] = make_uint4(0, 0, 0, 0);
         }
     }
-    float sum = 0.0f;
+    // a sum per vector and half of its words: chains of 4 terms, not one of 8 NV
+    float part[NV];
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
         uint32_t *p = reinterpret_cast<uint32_t *>(&v[i]);
@@ -70,14 +71,17 @@ __global__ __launch_bounds__(THREADS *ROWS) void rmsnorm_kernel(NormArgs a)
             if (live && c < a.H)
                 *reinterpret_cast<uint4 *>(a.residual_out + base + c) = v[i];
         }
+        float even = 0.0f, odd = 0.0f;
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             const float lo = dev::bf16_lo(p[j]), hi = dev::bf16_hi(p[j]);
-            sum = __builtin_fmaf(lo, lo, sum);
-            sum = __builtin_fmaf(hi, hi, sum);
+            even = __builtin_fmaf(lo, lo, even);
+            odd = __builtin_fmaf(hi, hi, odd);
         }
+        part[i] = even + odd;
     }
-    sum = wave_sum(sum);
+    static_assert(NV == 4, "pairs of pairs");
+    float sum = wave_sum((part[0] + part[1]) + (part[2] + part[3]));
     if constexpr (kWaves > 1) {
         if (lane == 0)
             red[sub][tid / kWave] = sum;

@@ -223,3 +223,21 @@ def test_products_of_cancelling_channels_stay_within_the_stated_bound(T, n, quan
     assert bool((err[::2] <= half_step[::2]).all()), "rows without loud channels"
     # every weight is loud (448) at the one loud channel of the other rows
     assert bool((err <= half_step + (1 + 2.0 ** -8) * 7 * 2.0 ** -13 * 448.0 ** 2).all())
+
+
+@pytest.mark.parametrize("H", [2048, 8192])
+def test_rmsnorm_keeps_small_squares_beside_large_ones(H):
+    """Every thread's first channel is 4096 and its 31 others 1: added one by one to 2^24 the ones are lost.
+
+    In fp32 the sum of a thread's four vectors may lose 3 of the 31 (a chain of four terms starts at 2^24); the
+    sums of threads are equal, so that adding them is exact.  Relative to the scale, in units of 2^-24: 1.5 for
+    those 3, half of one each for + eps and / H (under the root), one each for the root, the reciprocal, the
+    product with it, the division by 448 and the comparison: at most 7.5.  All 31 lost are 15.5."""
+    _say(f"rmsnorm, H={H}, squares of 2^24 and 1")
+    x = torch.ones(3, H, device="cuda")
+    x[:, 0:H // 4:8] = 4096.0
+    w = torch.ones(H, device="cuda").bfloat16()
+    _, _, s = _norm(x.bfloat16(), w, M.QUANT_FP8_F32)
+    y = x.double() / torch.sqrt(x.double().square().mean(-1, keepdim=True) + 1e-6)
+    want = y.unflatten(-1, (-1, 128)).amax(-1) / 448
+    assert float(((s.double() - want).abs() / want).max()) <= 8.5 * 2.0 ** -24
