@@ -29,16 +29,16 @@ __device__ __forceinline__ float wave_sum(float v)
 }
 
 // A row is handled by THREADS threads with up to NV vectors of 8 channels each
-// (H <= 8 * THREADS * NV); the block holds ROWS rows.
+// (H <= 8 * THREADS * NV); the block holds ROWS rows, the grid those from `first`.
 template <int QUANT, int THREADS, int ROWS, int NV>
-__global__ __launch_bounds__(THREADS *ROWS) void rmsnorm_kernel(NormArgs a)
+__global__ __launch_bounds__(THREADS *ROWS) void rmsnorm_kernel(NormArgs a, int64_t first)
 {
     constexpr int kWaves = THREADS / kWave;
     __shared__ float red[ROWS][kWaves];
     const int sub = ROWS == 1 ? 0 : threadIdx.x / THREADS;
     const int tid = threadIdx.x - sub * THREADS;
     const int lane = tid & (kWave - 1);
-    const int64_t t = (int64_t)blockIdx.x * ROWS + sub;
+    const int64_t t = first + (int64_t)blockIdx.x * ROWS + sub;
     const bool live = ROWS == 1 || t < a.T;
     const int nvec = a.H / 8;
     const int64_t base = t * a.H;
@@ -153,9 +153,17 @@ __global__ __launch_bounds__(THREADS *ROWS) void rmsnorm_kernel(NormArgs a)
 template <int QUANT, int THREADS, int ROWS, int NV>
 hipError_t launch(const NormArgs &a, hipStream_t stream)
 {
-    const dim3 grid((a.T + ROWS - 1) / ROWS), block(THREADS * ROWS);
-    hipLaunchKernelGGL((rmsnorm_kernel<QUANT, THREADS, ROWS, NV>), grid, block, 0, stream, a);
-    return hipGetLastError();
+    // A grid's threads are counted in 32 bits (past that it wraps, without an error).
+    constexpr int64_t kRows = ((int64_t)1 << 31) / THREADS;
+    for (int64_t first = 0; first < a.T; first += kRows) {
+        const int64_t rows = a.T - first < kRows ? a.T - first : kRows;
+        hipLaunchKernelGGL((rmsnorm_kernel<QUANT, THREADS, ROWS, NV>), dim3((uint32_t)((rows + ROWS - 1) / ROWS)),
+                           dim3(THREADS * ROWS), 0, stream, a, first);
+        const hipError_t e = hipGetLastError();
+        if (e != hipSuccess)
+            return e;
+    }
+    return hipSuccess;
 }
 
 template <int QUANT>

@@ -241,3 +241,26 @@ def test_rmsnorm_keeps_small_squares_beside_large_ones(H):
     y = x.double() / torch.sqrt(x.double().square().mean(-1, keepdim=True) + 1e-6)
     want = y.unflatten(-1, (-1, 128)).amax(-1) / 448
     assert float(((s.double() - want).abs() / want).max()) <= 8.5 * 2.0 ** -24
+
+
+# ---- large calls ------------------------------------------------------------------------------
+
+
+def test_rmsnorm_of_more_rows_than_a_grid_holds():
+    """64 threads a row: 2^26 rows are 2^32 threads, more than one launch takes."""
+    T, H = (1 << 26) + 5, 8
+    _say(f"rmsnorm, T={T}, H={H}")
+    base = torch.randn(4099, H, generator=_gen(1), device="cuda").bfloat16()
+    w = torch.randn(H, generator=_gen(2), device="cuda").bfloat16()
+    cfg = _cfg(4099, H, quant=M.QUANT_NONE)
+    want = _filled((4099, H), torch.bfloat16)
+    M.moe_rmsnorm(cfg, 4099, base, None, w, 1e-6, None, want)
+    x, out, n = torch.empty(T, H, dtype=torch.bfloat16, device="cuda"), _filled((T + 1, H), torch.bfloat16), T // 4099
+    x[:n * 4099].view(n, 4099, H).copy_(base)
+    x[n * 4099:].copy_(base[:T - n * 4099])
+    M.moe_rmsnorm(_cfg(T, H, quant=M.QUANT_NONE), T, x, None, w, 1e-6, None, out)
+    torch.cuda.synchronize()
+    for i in range(0, T, 4099):
+        m = min(4099, T - i)
+        assert torch.equal(out[i:i + m].view(torch.int16), want[:m].view(torch.int16)), i
+    assert bool((out[T:].view(torch.uint8) == 0xA5).all())
