@@ -598,6 +598,8 @@ def _row_scales(quant: int, t: Optional[torch.Tensor], dev: int, rows: int, n: i
         if t is not None:
             raise ValueError(f"{name} must be None without FP8 quantization")
         return None
+    if quant not in _ROW_SCALES:
+        return None  # the library refuses the config
     elem, cols = _ROW_SCALES[quant](n)
     return _arg(t, dev, elem, rows * cols, name)
 
@@ -684,13 +686,14 @@ def moe_layer_fused(cfg: MoeConfig, num_tokens: int, inter: int, topk_idx: torch
     for at most LAYER_MAX_TOKENS tokens, in two kernels."""
     dev, H, P, E = _device(stream), cfg.hidden, num_tokens * cfg.num_topk, cfg.num_experts
     elem = 2 if cfg.quant == QUANT_NONE else 1
-    ws_elem = workspace.element_size()
+    ws_elem = 0 if workspace is None else workspace.element_size()
+    ws_bytes = 0 if workspace is None else workspace.numel() * ws_elem
     code = _load().moe_layer_fused(
         ctypes.byref(cfg), num_tokens, inter, _arg(topk_idx, dev, 4, P, "topk_idx"),
         _arg(topk_w, dev, 4, P, "topk_w"), _arg(x, dev, 2, num_tokens * H, "x"),
         _arg(w13, dev, elem, E * 2 * inter * H, "w13"), _weight_scales(cfg, w13_scale, dev, 2 * inter, H, "w13_scale"),
         _arg(w2, dev, elem, E * H * inter, "w2"), _weight_scales(cfg, w2_scale, dev, H, inter, "w2_scale"),
-        _arg(workspace, dev, ws_elem, 0, "workspace"), workspace.numel() * ws_elem,
+        _arg(workspace, dev, ws_elem, 0, "workspace"), ws_bytes,
         _arg(out, dev, 2, num_tokens * H, "out"), _raw_stream(stream, dev))
     if code:
         raise MoeError("moe_layer_fused", code)

@@ -264,3 +264,40 @@ def test_rmsnorm_of_more_rows_than_a_grid_holds():
         m = min(4099, T - i)
         assert torch.equal(out[i:i + m].view(torch.int16), want[:m].view(torch.int16)), i
     assert bool((out[T:].view(torch.uint8) == 0xA5).all())
+
+
+# ---- refusals -----------------------------------------------------------------------------------
+
+
+def test_an_unknown_format_is_the_librarys_argument_error():
+    _say("expert-layer operators with cfg.quant = 7")
+    cfg = _cfg(4, 256, 2, 1, quant=7)
+    b16, b8 = torch.zeros(4, 256, device="cuda").bfloat16(), torch.zeros(4, 256, dtype=torch.uint8, device="cuda")
+    w = torch.zeros(2, 512, 256, dtype=torch.uint8, device="cuda")
+    s = torch.zeros(2048, device="cuda")
+    idx, tw = torch.zeros(4, 1, dtype=torch.int32, device="cuda"), torch.zeros(4, 1, device="cuda")
+    handle = M.Handle(_cfg(4, 256, 2, 1, quant=M.QUANT_NONE))
+    for call in (lambda: M.moe_rmsnorm(cfg, 4, b16, None, b16, 1e-6, None, b16, b8, s),
+                 lambda: M.moe_expert_gemm(cfg, 4, 256, 256, b8, s, w, s, handle, b16),
+                 lambda: M.moe_expert_gemm_swiglu(cfg, 4, 256, b8, s, w, s, handle, b8, s),
+                 lambda: M.moe_layer_fused(cfg, 4, 256, idx, tw, b16, w, s, w, s, w, b16)):
+        with pytest.raises(M.MoeError) as e:
+            call()
+        assert e.value.code == M.MOE_ERR_INVALID_ARG
+
+
+def test_no_token_needs_no_buffer():
+    _say("expert-layer operators without tokens or buffers")
+    cfg = _cfg(4, 256, quant=M.QUANT_FP8_F32)
+    w = torch.ones(256, device="cuda").bfloat16()
+    M.moe_rmsnorm(cfg, 0, None, None, w, 1e-6, None, None)
+    M.moe_expert_gemm(cfg, 0, 256, 256, None, None, None, None, None, None)
+    M.moe_expert_gemm_swiglu(cfg, 0, 256, None, None, None, None, None, None, None)
+    M.moe_layer_fused(cfg, 0, 256, None, None, None, None, None, None, None, None, None)
+    with pytest.raises(M.MoeError) as e:
+        x = torch.zeros(1, 256, device="cuda").bfloat16()
+        w8 = torch.zeros(1, 512, 256, dtype=torch.uint8, device="cuda")
+        one = torch.zeros(1, dtype=torch.int32, device="cuda")
+        M.moe_layer_fused(cfg, 1, 256, one, one, x, w8, torch.zeros(8, device="cuda"), w8,
+                          torch.zeros(8, device="cuda"), None, x)
+    assert e.value.code == M.MOE_ERR_INVALID_ARG
