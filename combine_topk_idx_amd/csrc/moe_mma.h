@@ -41,7 +41,8 @@ __device__ __forceinline__ void to_bf16(const u32x4 &v, float scale, bf16x8 &lo,
 // and at 64 + 16 g (hi) -- as four bf16 operands of v_mfma_f32_16x16x32_bf16,
 // times the block's scale where that is a power of two (`s`: as it is stored; the
 // word of four bytes for MXFP8, whose blocks g / 2 and 2 + g / 2 the lane has).
-// Byte 0, 2^-127, is taken as 0.
+// The conversion takes the scale's exponent field alone: byte 0 is 2^-127, 255 NaN.
+// Exact while the value fits bf16 (2^-133 .. 2^128): for bytes 3 .. 246 all do.
 template <int QUANT>
 __device__ __forceinline__ void block_to_bf16(const u32x4 &lo, const u32x4 &hi, uint32_t s, int g, bf16x8 v[4])
 {

@@ -35,6 +35,10 @@
  *              byte b%4 of word b/4 = exponent byte (2^(byte-127)) of block b
  *   MXFP8      w E4M3 [E, n, k], w_scale uint8 [E, n, k/32] (E8M0)
  *   NONE       w bf16 [E, n, k], w_scale NULL (moe_layer_fused only)
+ * Exponent byte 255 is NaN.  moe_layer_fused multiplies weights of UE8M0 and
+ * MXFP8 as the bf16 values they stand for: what lies below bf16's range is lost
+ * (bytes 0 to 2) or beyond it infinite (bytes from 247), the bytes between are
+ * exact.
  */
 #ifndef MOE_EXPERTS_H
 #define MOE_EXPERTS_H
@@ -55,7 +59,8 @@ extern "C" {
  *   residual_out = r, out = bf16(y),
  *   (out_q, out_scale) = y quantized as moe_dispatch quantizes (cfg.quant),
  *   from the fp32 y: one rounding to E4M3, not two.
- * The sum of squares is held in fp32.
+ * The sum of squares is held in fp32: where it overflows (an r of 2^64 and
+ * more) y is 0.
  *
  *   x             bf16 bits [num_tokens, H].
  *   residual      optional bf16 bits [num_tokens, H].

@@ -301,3 +301,69 @@ def test_no_token_needs_no_buffer():
         M.moe_layer_fused(cfg, 1, 256, one, one, x, w8, torch.zeros(8, device="cuda"), w8,
                           torch.zeros(8, device="cuda"), None, x)
     assert e.value.code == M.MOE_ERR_INVALID_ARG
+
+
+# ---- exponent bytes at their ends ------------------------------------------------------------------
+
+
+@pytest.mark.parametrize("quant", [M.QUANT_FP8_UE8M0, M.QUANT_MXFP8])
+@pytest.mark.parametrize("byte", [3, 4, 64, 190, 246, 255])
+def test_layer_weights_at_the_ends_of_their_exponents(byte, quant):
+    """Every finite E4M3 value times 2^(byte - 127) as a weight, beside an h of 2^-8 or 2^8: the exact product."""
+    _say(f"layer_fused, exponent byte {byte}, quant={quant}")
+    H = inter = 256
+    g0 = 16.0                                    # silu(16) = 16 (1 - 1.1e-7): bf16(16 u) exactly 16 u
+    u = 2.0 ** -4 * (2.0 ** 8 if byte < 127 else 2.0 ** -8)
+    w13 = torch.zeros(1, 2 * inter, H, dtype=torch.uint8, device="cuda")
+    w13[0, 0, 0] = w13[0, inter, 1] = 0x38       # 1: gate 0 = x[0], up 0 = x[1]
+    x = torch.zeros(1, H, device="cuda")
+    x[0, 0], x[0, 1] = g0, u
+    w2 = torch.zeros(1, H, inter, dtype=torch.uint8, device="cuda")
+    w2[0, :, 0] = torch.arange(256, dtype=torch.uint8, device="cuda")
+    w2[0, 0x7F, 0] = w2[0, 0xFF, 0] = 0          # NaN codes
+    n = {M.QUANT_MXFP8: lambda rows: (rows, inter // 32), M.QUANT_FP8_UE8M0: lambda rows: (rows // 128, 4)}[quant]
+    put = lambda b, rows: torch.full((1,) + n(rows), b, dtype=torch.uint8, device="cuda").view(  # noqa: E731
+        torch.uint8 if quant == M.QUANT_MXFP8 else torch.int32)
+    cfg = _cfg(1, H, quant=quant)
+    ws = _filled((M.moe_layer_workspace_bytes(cfg, inter),), torch.uint8)
+    out = _filled((1, H), torch.bfloat16)
+    M.moe_layer_fused(cfg, 1, inter, torch.zeros(1, 1, dtype=torch.int32, device="cuda"),
+                      torch.ones(1, 1, device="cuda"), x.bfloat16(), w13, put(127, 2 * inter), w2, put(byte, H), ws, out)
+    torch.cuda.synchronize()
+    if byte == 255:
+        assert bool(out.isnan().all())
+        return
+    want = w2[0, :, 0].view(R.F8).double() * 2.0 ** (byte - 127) * (g0 * u)
+    assert torch.equal(out[0].double(), want)     # four significant bits: no rounding
+
+
+@pytest.mark.parametrize("quant", [M.QUANT_FP8_UE8M0, M.QUANT_MXFP8])
+@pytest.mark.parametrize("byte", [0, 1, 127, 254, 255])
+@pytest.mark.parametrize("T,n", [(1, 256), (130, 256)])
+def test_product_weights_at_the_ends_of_their_exponents(T, n, byte, quant):
+    _say(f"expert_gemm, exponent byte {byte}, T={T}, quant={quant}")
+    k = 128
+    a = torch.zeros(T, k, dtype=torch.uint8, device="cuda")
+    a[:, 0] = 0x38
+    w = torch.zeros(1, n, k, dtype=torch.uint8, device="cuda")
+    w[0, :, 0] = torch.arange(256, dtype=torch.uint8, device="cuda")
+    w[0, 0x7F, 0] = w[0, 0xFF, 0] = 0
+    other = 254 - byte if byte < 255 else 127     # the rows' scale: the product's is 2^0
+    put = lambda b, rows: torch.full((rows, 4), b, dtype=torch.uint8, device="cuda").view(  # noqa: E731
+        torch.uint8 if quant == M.QUANT_MXFP8 else torch.int32)
+    y = _filled((T, n), torch.bfloat16)
+    M.moe_expert_gemm(_cfg(T, k, quant=quant), T, n, k, a, put(other, T), w,
+                      put(byte, n if quant == M.QUANT_MXFP8 else n // 128)[None], None, y)
+    torch.cuda.synchronize()
+    if byte == 255:
+        assert bool(y.isnan().all())
+    else:
+        assert torch.equal(y.double(), w[0, :, 0].view(R.F8).double().expand(T, n))
+
+
+def test_rmsnorm_whose_squares_overflow_gives_zero():
+    _say("rmsnorm of 2^64")
+    x = torch.ones(2, 256, device="cuda")
+    x[0, 3] = 2.0 ** 64
+    out, q, _ = _norm(x.bfloat16(), torch.ones(256, device="cuda").bfloat16(), M.QUANT_FP8_F32)
+    assert not bool(out[0].any()) and not bool((q[0] & 0x7F).any()) and bool(out[1].all())
