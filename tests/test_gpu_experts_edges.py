@@ -10,7 +10,7 @@ import torch
 
 import combine_topk_idx_amd as M
 import expert_reference as R
-from test_gpu_experts import _cfg, _filled, _gen, _gpu, _say, _scales  # noqa: F401 (_gpu: a fixture)
+from test_gpu_experts import Rows, _cfg, _filled, _gen, _gpu, _layer_reference, _say, _scales  # noqa: F401 (_gpu: a fixture)
 
 pytestmark = pytest.mark.gpu
 D = R.D
@@ -367,3 +367,248 @@ def test_rmsnorm_whose_squares_overflow_gives_zero():
     x[0, 3] = 2.0 ** 64
     out, q, _ = _norm(x.bfloat16(), torch.ones(256, device="cuda").bfloat16(), M.QUANT_FP8_F32)
     assert not bool(out[0].any()) and not bool((q[0] & 0x7F).any()) and bool(out[1].all())
+
+
+# ---- kernel variants that need many blocks, rows or channels -------------------------------------------
+
+
+def _dense_rows(T, k, quant, seed):
+    x = torch.randn(T, k, generator=_gen(seed), device="cuda")
+    x[::7] *= 100.0
+    return R.quantize(x, quant)
+
+
+def _check_product(y, a, s, w, ws, quant, what):
+    """Rows of bf16 against the 64-bit product: each value within its bound, all together within half a step."""
+    av = R.dequantize(a, s, quant)
+    wv = R.weight_values(w, ws, quant)[0]
+    want, bound = R.product(av, wv)
+    err = (y.to(D) - want).abs()
+    lim = (want.abs() + bound) * 2.0 ** -8 + bound
+    assert bool((err <= lim).all()), f"{what}: worst {float((err / lim).max()):.2f} times the bound"
+    # a bf16 rounding alone is at most 2^-8 of each value; 2^-15 for the 8-bit products (1.4e-5 measured)
+    assert float((y.to(D) - want).norm() / want.norm()) <= 2.0 ** -8 + 2.0 ** -15, what
+
+
+@pytest.mark.parametrize("quant", FORMATS)
+@pytest.mark.parametrize("k", [640, 1024, 1152, 1664])
+@pytest.mark.parametrize("T", [2304 + 40, 2304 + 100, 2304 + 200])
+def test_products_in_256_row_tiles_of_long_rows(T, k, quant):
+    """5, 8, 9 and 13 blocks of channels: the scales' chunks in turn and again, the loop with and without a last
+    step; last tiles of at most 64, 128 and 256 rows."""
+    n = 6664                                     # 10 row tiles x 27 channel tiles: more than the compute units
+    _say(f"expert_gemm T={T} k={k} n={n} quant={quant}")
+    a, s = _dense_rows(T, k, quant, T + k)
+    w, ws = R.make_weights(_gen(k), 1, n, k, quant, "cuda")
+    y = _filled((T + 1, n), torch.bfloat16)
+    M.moe_expert_gemm(_cfg(T, k, quant=quant), T, n, k, a, s, w, ws, None, y)
+    torch.cuda.synchronize()
+    assert bool((y[T:].view(torch.uint8) == 0xA5).all())
+    # rows of the first tile, of one inside and of the last
+    pick = torch.cat([torch.arange(0, 256, 17, device="cuda"), torch.arange(1280, 1536, 13, device="cuda"),
+                      torch.arange(2304, T, 9, device="cuda"), torch.tensor([T - 1], device="cuda")])
+    _check_product(y[pick], a[pick], s[pick], w, ws, quant, "picked rows")
+    # and all of them against fp32 sums of fp32 products
+    wv = R.weight_values(w, ws, quant)[0].float()
+    full = R.dequantize(a, s, quant).float() @ wv.T
+    assert float((y[:T].float() - full).norm() / full.norm()) <= 2.0 ** -8 + 2.0 ** -15
+
+
+def _check_swiglu(h, hs, a, s, w, ws, inter, quant, what):
+    av = R.dequantize(a, s, quant)
+    wv = R.weight_values(w, ws, quant)[0]
+    y, bound = R.product(av, wv, eight_bit=quant != M.QUANT_FP8_F32)
+    g, u, dg, du = y[:, :inter], y[:, inter:], bound[:, :inter], bound[:, inter:]
+    want = R.silu(g) * u
+    # |silu'| <= 1.1; the function itself in fp32 (an exponential of argument g: |g| ulps)
+    lim = 1.1 * dg * (u.abs() + du) + R.silu(g).abs() * du + want.abs() * (8 + g.abs()) * 2.0 ** -24
+    R.assert_rows(h, hs, want, lim, quant, what)
+    if quant == M.QUANT_FP8_F32:
+        ref = R.block_scale(want.abs().unflatten(-1, (-1, 128)).amax(-1), quant)
+        assert float((hs.to(D) - ref).norm() / ref.norm()) <= 1e-5, what
+    # E4M3 as a whole: 2^-4 of each value at most (MXFP8 saturates a block's largest by up to 1/8)
+    own = R.dequantize(h, hs, quant)
+    assert float((own - want).norm() / want.norm()) <= (2.0 ** -3 if quant == M.QUANT_MXFP8 else 2.0 ** -4), what
+
+
+@pytest.mark.parametrize("quant", FORMATS)
+@pytest.mark.parametrize("T,k,inter", [(100, 1152, 256), (45, 1664, 128), (300, 7168, 256), (20, 7168, 128)])
+def test_swiglu_of_long_rows(T, k, inter, quant):
+    _say(f"expert_gemm_swiglu T={T} k={k} inter={inter} quant={quant}")
+    a, s = _dense_rows(T, k, quant, T + k)
+    w, ws = R.make_weights(_gen(k), 1, 2 * inter, k, quant, "cuda")
+    h, hs = _filled((T, inter), torch.uint8), _scales(T, inter, quant)
+    M.moe_expert_gemm_swiglu(_cfg(T, k, quant=quant), T, inter, a, s, w, ws, None, h, hs)
+    torch.cuda.synchronize()
+    _check_swiglu(h, hs, a, s, w, ws, inter, quant, "all rows")
+
+
+@pytest.mark.parametrize("quant", FORMATS)
+def test_swiglu_of_many_small_tiles_from_memory(quant):
+    """Blocks that go from tile to tile, a few rows of another expert each, with caches cold."""
+    T, E, K, k, inter = 96, 64, 6, 1024, 2048
+    _say(f"expert_gemm_swiglu of many small tiles, caches cold, quant={quant}")
+    rows = Rows(15, quant=quant, T=T, E=E, K=K, k=k)
+    w, ws = R.make_weights(_gen(16), E, 2 * inter, k, quant, "cuda")
+    cold = torch.empty(1 << 29, dtype=torch.uint8, device="cuda")
+    h, hs = _filled((rows.rows, inter), torch.uint8), _scales(rows.rows, inter, quant)
+    cold.fill_(1)
+    M.moe_expert_gemm_swiglu(rows.cfg, T, inter, rows.a, rows.s, w, ws, rows.handle, h, hs)
+    torch.cuda.synchronize()
+    for e in (0, 13, 21, 42, 63):
+        at = slice(rows.off[e], rows.off[e] + rows.count[e])
+        _check_swiglu(h[at], hs[at], rows.a[at], rows.s[at], w[e:e + 1], ws[e:e + 1], inter, quant, f"expert {e}")
+
+
+LAYERS = [
+    # 32 channels of h per block (eight blocks per compute unit), one and two groups of 16 tokens
+    dict(T=16, E=64, K=4, H=256, inter=1024),
+    dict(T=24, E=64, K=4, H=256, inter=1024),
+    dict(T=32, E=2, K=1, H=128, inter=32768),    # more than 16 tokens of one expert
+    dict(T=40, E=64, K=4, H=256, inter=1024),
+    # 32 output channels per block (H past 16 per compute unit), two and four groups
+    dict(T=20, E=6, K=2, H=4224, inter=128),
+    dict(T=32, E=1, K=1, H=4224, inter=256),
+    dict(T=40, E=6, K=2, H=4224, inter=128),
+    dict(T=64, E=1, K=1, H=4224, inter=256),
+]
+
+
+@pytest.mark.parametrize("quant", [M.QUANT_NONE] + FORMATS)
+@pytest.mark.parametrize("c", LAYERS, ids=lambda c: "T{T}_E{E}_K{K}_H{H}_i{inter}".format(**c))
+def test_layer_fused_in_wide_blocks(c, quant):
+    _say(f"layer_fused {c} quant={quant}")
+    T, E, K, H, inter = c["T"], c["E"], c["K"], c["H"], c["inter"]
+    g = _gen(T + E + H)
+    idx = torch.topk(torch.rand(T, E, generator=g, device="cuda"), K, 1).indices.to(torch.int32)
+    if K > 1:
+        idx[3, 1] = -1
+        idx[5, 1] = idx[5, 0]
+    tw = torch.rand(T, K, generator=g, device="cuda")
+    tw[idx < 0] = NAN
+    x = torch.randn(T, H, generator=g, device="cuda").bfloat16()
+    w13, s13 = R.make_weights(g, E, 2 * inter, H, quant, "cuda")
+    w2, s2 = R.make_weights(g, E, H, inter, quant, "cuda")
+    cfg = _cfg(T, H, E, K, quant)
+    ws = _filled((M.moe_layer_workspace_bytes(cfg, inter),), torch.uint8)
+    out = _filled((T + 1, H), torch.bfloat16)
+    M.moe_layer_fused(cfg, T, inter, idx, tw, x, w13, s13, w2, s2, ws, out)
+    torch.cuda.synchronize()
+    assert bool((out[T:].view(torch.uint8) == 0xA5).all())
+    want, bound = _layer_reference(idx, tw, x, w13, s13, w2, s2, quant, inter)
+    err = (out[:T].to(D) - want).abs()
+    lim = (want.abs() + bound) * 2.0 ** -8 + bound
+    assert bool((err <= lim).all()), float((err / lim).max())
+    # both roundings of half a step, as a whole
+    assert float((out[:T].to(D) - want).norm()) <= 2.0 ** -7 * float(want.norm())
+
+
+# ---- weights past 4 GiB --------------------------------------------------------------------------------
+# One row of the last expert; the weights of the others are never read (whatever the memory held).
+
+
+def _last_expert(E, n, k, quant, seed):
+    w1, s1 = R.make_weights(_gen(seed), 1, n, k, quant, "cuda")
+    w = torch.empty(E, n, k, dtype=torch.uint8, device="cuda")
+    s = torch.empty((E,) + tuple(s1.shape[1:]), dtype=s1.dtype, device="cuda")
+    w[E - 1], s[E - 1] = w1[0], s1[0]
+    return w, s, w1, s1
+
+
+def _one_row(E, k, quant):
+    cfg = _cfg(1, k, E, 1, quant)
+    handle = M.Handle(cfg)
+    lw = torch.empty(M.moe_workspace_bytes(cfg), dtype=torch.uint8, device="cuda")
+    idx = torch.full((1, 1), E - 1, dtype=torch.int32, device="cuda")
+    M.moe_dispatch_layout(cfg, 1, idx, handle, lw)
+    a, s = _dense_rows(1, k, quant, k)
+    return cfg, handle, idx, a, s
+
+
+@pytest.mark.parametrize("quant", FORMATS)
+def test_strips_read_weights_past_4_gib(quant):
+    E, n, k = 2048, 128, 16512                    # 8 strips of 16 channels: fewer than the chip takes at once
+    _say(f"expert_gemm, {E * n * k} bytes of weights, the last expert, quant={quant}")
+    w, ws, w1, ws1 = _last_expert(E, n, k, quant, 3)
+    cfg, handle, _, a, s = _one_row(E, k, quant)
+    y = _filled((1, n), torch.bfloat16)
+    M.moe_expert_gemm(cfg, 1, n, k, a, s, w, ws, handle, y)
+    torch.cuda.synchronize()
+    _check_product(y, a, s, w1, ws1, quant, "the last expert")
+
+
+@pytest.mark.parametrize("quant", FORMATS)
+def test_tiles_read_weights_past_4_gib(quant):
+    E, n, k = 33, 16384, 8192                     # 1024 strips: 128-row tiles
+    _say(f"expert_gemm, {E * n * k} bytes of weights, the last expert, quant={quant}")
+    w, ws, w1, ws1 = _last_expert(E, n, k, quant, 4)
+    cfg, handle, _, a, s = _one_row(E, k, quant)
+    y = _filled((1, n), torch.bfloat16)
+    M.moe_expert_gemm(cfg, 1, n, k, a, s, w, ws, handle, y)
+    torch.cuda.synchronize()
+    _check_product(y, a, s, w1, ws1, quant, "the last expert")
+
+
+@pytest.mark.parametrize("quant", FORMATS)
+def test_swiglu_reads_weights_past_4_gib(quant):
+    E, inter, k = 2048, 128, 8320
+    _say(f"expert_gemm_swiglu, {E * 2 * inter * k} bytes of weights, the last expert, quant={quant}")
+    w, ws, w1, ws1 = _last_expert(E, 2 * inter, k, quant, 5)
+    cfg, handle, _, a, s = _one_row(E, k, quant)
+    h, hs = _filled((1, inter), torch.uint8), _scales(1, inter, quant)
+    M.moe_expert_gemm_swiglu(cfg, 1, inter, a, s, w, ws, handle, h, hs)
+    torch.cuda.synchronize()
+    _check_swiglu(h, hs, a, s, w1, ws1, inter, quant, "the last expert")
+
+
+@pytest.mark.parametrize("quant", FORMATS)
+def test_layer_reads_weights_past_4_gib(quant):
+    E, inter, H = 2048, 256, 8320
+    _say(f"layer_fused, {E * inter * H} bytes of w2, the last expert, quant={quant}")
+    w13, s13, w13e, s13e = _last_expert(E, 2 * inter, H, quant, 6)
+    w2, s2, w2e, s2e = _last_expert(E, H, inter, quant, 7)
+    cfg, _, idx, _, _ = _one_row(E, H, quant)
+    x = torch.randn(1, H, generator=_gen(8), device="cuda").bfloat16()
+    tw = torch.full((1, 1), 0.7, device="cuda")
+    ws = _filled((M.moe_layer_workspace_bytes(cfg, inter),), torch.uint8)
+    out = _filled((1, H), torch.bfloat16)
+    M.moe_layer_fused(cfg, 1, inter, idx, tw, x, w13, s13, w2, s2, ws, out)
+    torch.cuda.synchronize()
+    want, bound = _layer_reference(torch.zeros_like(idx), tw, x, w13e, s13e, w2e, s2e, quant, inter)
+    err = (out.to(D) - want).abs()
+    lim = (want.abs() + bound) * 2.0 ** -8 + bound
+    assert bool((err <= lim).all()), float((err / lim).max())
+    assert float((out.to(D) - want).norm()) <= 2.0 ** -7 * float(want.norm())
+
+
+@pytest.mark.parametrize("quant", [M.QUANT_NONE] + FORMATS)
+@pytest.mark.parametrize("T,E", [(3, 16), (40, 4)])
+def test_layer_with_a_token_that_is_not_finite(T, E, quant):
+    """NaN or infinity in one token, NaN in another's weights: the other tokens' bytes are as without them."""
+    _say(f"layer_fused T={T} E={E}, tokens that are not finite, quant={quant}")
+    K, H, inter = 2, 512, 256
+    g = _gen(T)
+    idx = torch.topk(torch.rand(T, E, generator=g, device="cuda"), K, 1).indices.to(torch.int32)
+    tw = torch.rand(T, K, generator=g, device="cuda")
+    x = torch.randn(T, H, generator=g, device="cuda").bfloat16()
+    w13, s13 = R.make_weights(g, E, 2 * inter, H, quant, "cuda")
+    w2, s2 = R.make_weights(g, E, H, inter, quant, "cuda")
+    cfg = _cfg(T, H, E, K, quant)
+    ws = _filled((M.moe_layer_workspace_bytes(cfg, inter),), torch.uint8)
+
+    def run(x, tw):
+        out = _filled((T, H), torch.bfloat16)
+        M.moe_layer_fused(cfg, T, inter, idx, tw, x, w13, s13, w2, s2, ws, out)
+        torch.cuda.synchronize()
+        return out
+
+    clean = run(x, tw)
+    assert bool(clean.isfinite().all())
+    for value in (NAN, INF):
+        bad, weights = x.clone(), tw.clone()
+        bad[1, 7] = value
+        weights[2, 1] = NAN
+        got = run(bad, weights)
+        rest = [t for t in range(T) if t not in (1, 2)]
+        _bytes_equal(got[rest], clean[rest], "another token")
+        assert bool(got[2].isnan().all()) and bool((~got[1].isfinite()).any())
