@@ -7,12 +7,16 @@
 // Both are bound by the weights of the experts that the batch reaches, each
 // byte of which is read once: a wave streams 16 weight rows straight from
 // memory into matrix-instruction operands, converting 8-bit values to bf16 on
-// the way (exact), and the activations stay bf16.  Tokens are the columns of
-// the product.  gate_up has a block per (expert, 16 channels of h); down has a
-// block per 16 output channels that walks every expert, with a zero column
-// where a token does not use the expert, so that the weighted sum over a
-// token's experts is the accumulation itself, in a fixed order and without
-// atomics.
+// the way (exact), and the activations stay bf16.  Between the kernels h is
+// bf16 too, as the definition says: the operand of the second product, and the
+// one rounding between x and out (half a step, 2^-8, of each value: the output
+// is 2.3e-3 off, rms, instead of the 1.7e-3 of its own rounding).
+//
+// Tokens are the columns of the products: an expert's tokens are packed into
+// groups of 16.  gate_up has a block per (expert, 16 or 32 channels of h); down has
+// a block per 16 or 32 output channels that walks every expert used and adds each
+// one's columns, times the router's weight, to its tokens' sums in LDS, per wave
+// and at last over the waves in a fixed order, without atomics.
 #include "moe_mma.h"
 
 namespace moe {
@@ -422,11 +426,16 @@ hipError_t launch_groups(const LayerArgs &a, hipStream_t stream)
     const int32_t slots = layer_slots(a.T * a.K, a.E);
     const int32_t cus = device_cu_count();
     // 32 channels of h per block read x half as often, where enough blocks are left.
-    // Whole layer, 16 / 32 channels: 48 tokens, 64 experts, 7168 -> 2048: 542 / 516 us;
-    // 16 tokens, 32 experts, 4096 -> 1536: 114 / 120; 5 tokens: 55.3 / 56.6.
-    if ((int64_t)slots * (a.I / 32) >= 8 * cus)
-        hipLaunchKernelGGL((layer_gate_up<QUANT, G, 2>), dim3(a.I / 32, slots), dim3(kLayerWaves * kWave), 0, stream,
-                           a);
+    // Whole layer, 7168 -> 2048, 64 experts, top 8, 16 / 32 channels: 48 tokens fp32
+    // scales 543 / 520 us, UE8M0 528 / 497, MXFP8 666 / 666; 64 tokens 587 / 547, 567 /
+    // 521, 704 / 694; 24 tokens 451 / 450, 456 / 450, 574 / 564.  With fewer blocks 16
+    // tokens, 32 experts, 4096 -> 1536: 127 / 130, 128 / 131, 149 / 145.  MXFP8 spills 6
+    // registers there.  bf16 weights would spill 66: 48 tokens 969 / 1052 us, 64 tokens
+    // 990 / 1065, 8 tokens 631 / 636.
+    constexpr int kWide = QUANT == MOE_QUANT_NONE ? 1 : 2;
+    if (kWide > 1 && (int64_t)slots * (a.I / (16 * kWide)) >= 8 * cus)
+        hipLaunchKernelGGL((layer_gate_up<QUANT, G, kWide>), dim3(a.I / (16 * kWide), slots),
+                           dim3(kLayerWaves * kWave), 0, stream, a);
     else
         hipLaunchKernelGGL((layer_gate_up<QUANT, G, 1>), dim3(a.I / 16, slots), dim3(kLayerWaves * kWave), 0, stream,
                            a);
