@@ -89,8 +89,7 @@ __device__ inline void scan_tiles(const ExpertGemmArgs &p, int32_t *tile_start, 
     __syncthreads();
 }
 
-// An expert's rows: `first` of them lie in tiles before, its tiles start at
-// number `start`.
+// An expert, the number of its first row tile and of its rows.
 struct ExpertAt {
     int32_t e, start, rows;
 };
@@ -173,8 +172,8 @@ __device__ __forceinline__ void write_tile(const ExpertGemmArgs &p, dev::f32x4 (
         // the row's 64.  The other half comes from the lane 8 further, for the
         // half that one needs: a store then covers whole cache lines, 128 bytes of
         // each of 8 rows.  Rows and channels past the end go past the buffer's,
-        // which drops them.  The stores are marked as streamed (non-temporal), which leaves L2 to the weights (8192
-        // dense rows, 7168 -> 8192, UE8M0: 424 -> 382 us).
+        // which drops them.  The stores are marked as streamed (non-temporal), which
+        // leaves L2 to the weights (8192 dense rows, 7168 -> 8192, UE8M0: 424 -> 382 us).
         constexpr int kStreamed = 2;
         const __amdgpu_buffer_rsrc_t out = buffer(p.y + at.row0 * p.n, (uint32_t)at.valid * (uint32_t)p.n * 2);
         const bool low = r < 8;
@@ -825,8 +824,10 @@ hipError_t launch_rows(const ExpertGemmArgs &p, hipStream_t stream)
             return hipGetLastError();
         }
         // 256-row tiles read the weights half as often, with one stage less in flight
-        // and larger remainders: plain product, 2048 -> 7168, 64 experts, UE8M0, 128 /
-        // 256 rows: 256 rows per expert 376 / 397 us, 512: 630 / 616, 1024: 1183 / 1068.
+        // and larger remainders.  2048 -> 7168, 64 experts, 128 / 256 rows: 256 rows per
+        // expert fp32 scales 421 / 446 us, UE8M0 376 / 387, MXFP8 390 / 427; 512: 683 /
+        // 668, 631 / 613, 642 / 644; 1024: 1243 / 1199, 1168 / 1059, 1214 / 1114 (the 256-row
+        // kernels of fp32 scales and MXFP8 spill 8 and 15 registers).
         // For SwiGLU (7168 -> 2 x 2048) 512: 1099 / 1201, 768: 1536 / 1654, 1024: 1996 /
         // 1977, and the registers spill.  Fewer tiles than compute units: 128 rows.
         if (p.max_rows / p.E >= 512 && max_tiles(p, 256) * ((p.n + kTileN - 1) / kTileN) >= cus)

@@ -172,7 +172,10 @@ hipError_t launch_quant(const NormArgs &a, hipStream_t stream)
     // A wave per row without a barrier, four rows per block, or four waves per row:
     // 8192 rows of 1024 channels 14.6 / 26.0 us, of 2048 32.6 / 32.5.  More threads
     // than the row needs leave lanes idle: 16 waves for 7168 channels 262 us at 16,384
-    // rows, four 187 (5.1 TB/s; one row: 3.7 us, launch and two dependent round trips).
+    // rows, four 187 (5.7 TB/s; one row: 3.7 us, launch and two dependent round trips).
+    // Past 8192 channels a row needs the registers of more than four waves: 4096 rows of
+    // 32,768 channels 230 us (5.3 TB/s), of 16,384 126 (4.8), of 12,288 101 (4.5), of
+    // 8320, which fill half the lanes, 80 (3.8).
     if (a.H <= 2048)
         return launch<QUANT, 64, 4, 4>(a, stream);
     if (a.H <= 8192)
