@@ -14,7 +14,7 @@
 // Bounds and measurements (one MI355X; times of calls in a row):
 //   a few rows in all: latency (expert_gemm_strips).  One row, 7168 -> 7168: 15 us;
 //   few rows per expert: the weights' bytes.  128 experts x 8 rows, 768 -> 2048:
-//   45 us; 256 experts x 8 rows, 7168 -> 2 x 2048, SwiGLU: 1.23 ms, 6.1 TB/s;
+//   45 us; 256 experts x 8 rows, 7168 -> 2 x 2048, SwiGLU: 1.27 ms, 5.9 TB/s;
 //   many rows: the matrix cores and LDS.  8192 dense rows, 7168 -> 8192, UE8M0:
 //   383 us, 2510 TFLOP/s (a library's product of 8192^3 with one scale: 2718);
 //   in between: the start and end of a tile (a block's results leave while nothing

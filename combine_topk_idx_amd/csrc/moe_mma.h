@@ -16,7 +16,7 @@ typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 
 constexpr bool per_row_weight_scale(int quant) { return quant == MOE_QUANT_MXFP8; }
 
-// fp32 -> bf16 bits, round to nearest even (finite values and infinities).
+// fp32 -> bf16 bits, round to nearest even; infinities and NaN stay what they are.
 __device__ __forceinline__ uint32_t bf16_bits(float f)
 {
     return __builtin_bit_cast(uint16_t, (__bf16)f);
