@@ -75,8 +75,10 @@ moe_status_t check_layer(const moe_config_t *cfg, int32_t inter)
     const moe_status_t st = check_config(cfg);
     if (st != MOE_OK)
         return st;
-    if (inter < kQuantGroup || inter % kQuantGroup != 0 || inter > INT32_MAX / 2 || cfg->hidden % kQuantGroup != 0)
+    if (inter < kQuantGroup || inter % kQuantGroup != 0 || cfg->hidden % kQuantGroup != 0)
         return MOE_ERR_INVALID_ARG;
+    if (inter > kMaxLayerChannels || cfg->hidden > kMaxLayerChannels)
+        return MOE_ERR_UNSUPPORTED;
     return MOE_OK;
 }
 

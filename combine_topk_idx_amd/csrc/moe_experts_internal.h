@@ -50,6 +50,10 @@ hipError_t launch_expert_gemm(const ExpertGemmArgs &a, int32_t quant, bool swigl
 
 // ---- few-token layer --------------------------------------------------------------
 
+// Channels of the layer, inner or outer: its grids' threads (16 or 32 channels per
+// block of 256 or 512) are counted in 32 bits and would wrap without an error.
+constexpr int32_t kMaxLayerChannels = 1 << 27;
+
 struct LayerArgs {
     const int32_t *topk_idx;
     const float *topk_w;

@@ -132,8 +132,8 @@ moe_status_t moe_expert_gemm_swiglu(const moe_config_t *cfg, int32_t num_tokens,
                                     const moe_handle_t *handle, void *h, void *h_scale, void *stream);
 
 /* Bytes of device workspace moe_layer_fused needs for up to cfg.max_tokens
- * tokens (at most MOE_LAYER_MAX_TOKENS per call).  Returns 0 for an invalid
- * config or inter. */
+ * tokens (at most MOE_LAYER_MAX_TOKENS per call).  Returns 0 for a config or
+ * inter that it refuses. */
 size_t moe_layer_workspace_bytes(const moe_config_t *cfg, int32_t inter);
 
 /*
@@ -146,7 +146,8 @@ size_t moe_layer_workspace_bytes(const moe_config_t *cfg, int32_t inter);
  * moe_dispatch_layout (their weight is not read); a token without pairs gives
  * +0.  The same expert twice in one token counts twice.
  *
- *   inter      a multiple of 128; cfg.hidden too, for every format.
+ *   inter      a multiple of 128, at most 2^27 (larger: MOE_ERR_UNSUPPORTED);
+ *              cfg.hidden too, for every format.
  *   topk_idx   int32 [num_tokens, K]; topk_w fp32 [num_tokens, K].
  *   x          bf16 bits [num_tokens, H].
  *   w13        [E, 2*inter, H] (gate rows first), w2 [E, H, inter].
