@@ -1,8 +1,9 @@
 """MI355X (gfx950) MoE token dispatch / combine.
 
 A thin ctypes binding over ``libmoe_dispatch.so`` (HIP kernels behind the C
-ABI declared in ``include/moe_dispatch.h`` and, for the expert layer's
-operators, ``include/moe_experts.h``).  The Python functions carry the
+ABI declared in ``include/moe_dispatch.h``, for the expert layer's operators
+``include/moe_experts.h`` and, for the bf16 layer with its gradients,
+``include/moe_train.h``).  The Python functions carry the
 same names as the C entry points and only marshal arguments: torch tensors
 supply device memory and the current HIP stream, and every step of the path
 runs in the library's kernels.  There is no fallback: if the library is not
@@ -42,6 +43,10 @@ QUANT_NONE = 0
 QUANT_FP8_F32 = 1
 QUANT_FP8_UE8M0 = 2
 QUANT_MXFP8 = 3
+ACT_NONE = 0
+ACT_SILU = 1
+ACT_GELU = 2
+ACT_RELU = 3
 
 
 class MoeError(RuntimeError):
@@ -144,6 +149,20 @@ def _load():
     lib.moe_layer_workspace_bytes.restype = sz
     lib.moe_layer_fused.argtypes = [cfgp, i32, i32, P, P, P, P, P, P, P, P, sz, P, P]
     lib.moe_layer_fused.restype = ctypes.c_int
+    lib.moe_ffn_gated.argtypes = [cfgp, i32, i32, i32, P, P, hp, P, P, P, i32, P]
+    lib.moe_ffn_gated.restype = ctypes.c_int
+    lib.moe_expert_linear.argtypes = [cfgp, i32, i32, i32, i32, P, P, P, P, hp, P, P, P, i32, P]
+    lib.moe_expert_linear.restype = ctypes.c_int
+    lib.moe_activation_backward.argtypes = [cfgp, i32, i32, i32, i32, P, P, P, i32, hp, P, P, P]
+    lib.moe_activation_backward.restype = ctypes.c_int
+    lib.moe_expert_grad_input.argtypes = [cfgp, i32, i32, i32, P, P, hp, P, P]
+    lib.moe_expert_grad_input.restype = ctypes.c_int
+    lib.moe_grad_weight_workspace_bytes.argtypes = [cfgp, i32, i32, i32]
+    lib.moe_grad_weight_workspace_bytes.restype = sz
+    lib.moe_expert_grad_weight.argtypes = [cfgp, i32, i32, i32, P, P, P, i32, hp, P, i32, P, i32, P, sz, P]
+    lib.moe_expert_grad_weight.restype = ctypes.c_int
+    lib.moe_combine_backward.argtypes = [cfgp, i32, P, P, P, hp, P, P, P]
+    lib.moe_combine_backward.restype = ctypes.c_int
     lib.moe_status_str.argtypes = [ctypes.c_int]
     lib.moe_status_str.restype = ctypes.c_char_p
     _lib = lib
@@ -697,3 +716,125 @@ def moe_layer_fused(cfg: MoeConfig, num_tokens: int, inter: int, topk_idx: torch
         _arg(out, dev, 2, num_tokens * H, "out"), _raw_stream(stream, dev))
     if code:
         raise MoeError("moe_layer_fused", code)
+
+
+# ---- the expert layer in bf16 with its gradients (include/moe_train.h) -------------
+
+def _rows_of(cfg, num_tokens: int, handle: Optional[Handle], dev: int):
+    """Rows of a call, and the handle's struct: the dispatched rows, or num_tokens dense ones."""
+    if handle is None:
+        return num_tokens, None
+    rows = moe_rows_capacity(cfg)
+    _arg(handle.recv_count, dev, 4, cfg.num_experts, "handle")
+    _arg(handle.row_to_pair, dev, 4, rows, "handle")
+    return rows, ctypes.byref(handle.c)
+
+
+def _formatted(quant: int, t, scale, dev: int, rows: int, n: int, name: str):
+    """Addresses of rows of n channels in a format (bf16 or 8 bits) and of their scales."""
+    if t is None:
+        if scale is not None:
+            raise ValueError(f"{name}_scale without {name}")
+        return None, None
+    return (_arg(t, dev, 2 if quant == QUANT_NONE else 1, rows * n, name),
+            _row_scales(quant, scale, dev, rows, n, name + "_scale"))
+
+
+def moe_ffn_gated(cfg: MoeConfig, num_tokens: int, inter: int, act: int, a: torch.Tensor, w13: torch.Tensor,
+                  handle: Optional[Handle], h: torch.Tensor, saved: Optional[torch.Tensor] = None,
+                  saved_scale: Optional[torch.Tensor] = None, saved_quant: int = QUANT_NONE, stream=None) -> None:
+    """h[row] = bf16(act(gate) * up) with gate and up the halves of a[row] @ w13[e].T,
+    which `saved` keeps for the gradient (bf16, or 8 bits with scales)."""
+    dev, H = _device(stream), cfg.hidden
+    rows, hp = _rows_of(cfg, num_tokens, handle, dev)
+    sp, ssp = _formatted(saved_quant, saved, saved_scale, dev, rows, 2 * inter, "saved")
+    code = _load().moe_ffn_gated(
+        ctypes.byref(cfg), num_tokens, inter, act, _arg(a, dev, 2, rows * H, "a"),
+        _arg(w13, dev, 2, cfg.num_experts * 2 * inter * H, "w13"), hp, _arg(h, dev, 2, rows * inter, "h"), sp, ssp,
+        saved_quant, _raw_stream(stream, dev))
+    if code:
+        raise MoeError("moe_ffn_gated", code)
+
+
+def moe_expert_linear(cfg: MoeConfig, num_tokens: int, n: int, k: int, act: int, a: torch.Tensor, w: torch.Tensor,
+                      bias: Optional[torch.Tensor], residual: Optional[torch.Tensor], handle: Optional[Handle],
+                      y: torch.Tensor, saved: Optional[torch.Tensor] = None,
+                      saved_scale: Optional[torch.Tensor] = None, saved_quant: int = QUANT_NONE, stream=None) -> None:
+    """y[row] = bf16(act(p) + residual[row]) with p = a[row] @ w[e].T + bias[e], which
+    `saved` keeps for the gradient (bf16, or 8 bits with scales)."""
+    dev, E = _device(stream), cfg.num_experts
+    rows, hp = _rows_of(cfg, num_tokens, handle, dev)
+    sp, ssp = _formatted(saved_quant, saved, saved_scale, dev, rows, n, "saved")
+    code = _load().moe_expert_linear(
+        ctypes.byref(cfg), num_tokens, n, k, act, _arg(a, dev, 2, rows * k, "a"), _arg(w, dev, 2, E * n * k, "w"),
+        _arg(bias, dev, 2, E * n, "bias"), _arg(residual, dev, 2, rows * n, "residual"), hp,
+        _arg(y, dev, 2, rows * n, "y"), sp, ssp, saved_quant, _raw_stream(stream, dev))
+    if code:
+        raise MoeError("moe_expert_linear", code)
+
+
+def moe_activation_backward(cfg: MoeConfig, num_tokens: int, n: int, act: int, gated: bool, dy: torch.Tensor,
+                            saved: torch.Tensor, saved_scale: Optional[torch.Tensor], saved_quant: int,
+                            handle: Optional[Handle], dsaved: torch.Tensor, y: Optional[torch.Tensor] = None,
+                            stream=None) -> None:
+    """Gradient of act(saved), or (gated) of act(gate) * up, to its saved input; y:
+    the output again."""
+    dev, m = _device(stream), 2 * n if gated else n
+    rows, hp = _rows_of(cfg, num_tokens, handle, dev)
+    sp, ssp = _formatted(saved_quant, saved, saved_scale, dev, rows, m, "saved")
+    code = _load().moe_activation_backward(
+        ctypes.byref(cfg), num_tokens, n, act, int(bool(gated)), _arg(dy, dev, 2, rows * n, "dy"), sp, ssp, saved_quant,
+        hp, _arg(dsaved, dev, 2, rows * m, "dsaved"), _arg(y, dev, 2, rows * n, "y"), _raw_stream(stream, dev))
+    if code:
+        raise MoeError("moe_activation_backward", code)
+
+
+def moe_expert_grad_input(cfg: MoeConfig, num_tokens: int, n: int, k: int, dy: torch.Tensor, w: torch.Tensor,
+                          handle: Optional[Handle], da: torch.Tensor, stream=None) -> None:
+    """da[row] = dy[row] @ w[e]: the gradient of a[row] @ w[e].T to a."""
+    dev = _device(stream)
+    rows, hp = _rows_of(cfg, num_tokens, handle, dev)
+    code = _load().moe_expert_grad_input(
+        ctypes.byref(cfg), num_tokens, n, k, _arg(dy, dev, 2, rows * n, "dy"),
+        _arg(w, dev, 2, cfg.num_experts * n * k, "w"), hp, _arg(da, dev, 2, rows * k, "da"), _raw_stream(stream, dev))
+    if code:
+        raise MoeError("moe_expert_grad_input", code)
+
+
+def moe_grad_weight_workspace_bytes(cfg: MoeConfig, num_tokens: int, n: int, k: int) -> int:
+    return int(_load().moe_grad_weight_workspace_bytes(ctypes.byref(cfg), int(num_tokens), int(n), int(k)))
+
+
+def moe_expert_grad_weight(cfg: MoeConfig, num_tokens: int, n: int, k: int, dy: torch.Tensor, a: torch.Tensor,
+                           a_scale: Optional[torch.Tensor], a_quant: int, handle: Optional[Handle], dw: torch.Tensor,
+                           dbias: Optional[torch.Tensor] = None, accumulate: bool = False,
+                           workspace: Optional[torch.Tensor] = None, stream=None) -> None:
+    """dw[e] = dy[rows of e].T @ a[rows of e] (fp32 or bf16, by dw's element size) and
+    dbias[e] = dy[rows of e].sum(0), written or (accumulate, fp32) added."""
+    dev, E = _device(stream), cfg.num_experts
+    rows, hp = _rows_of(cfg, num_tokens, handle, dev)
+    ap, asp = _formatted(a_quant, a, a_scale, dev, rows, k, "a")
+    elem = 4 if dw is None or dw.element_size() == 4 else 2
+    ws_elem = 0 if workspace is None else workspace.element_size()
+    ws_bytes = 0 if workspace is None else workspace.numel() * ws_elem
+    code = _load().moe_expert_grad_weight(
+        ctypes.byref(cfg), num_tokens, n, k, _arg(dy, dev, 2, rows * n, "dy"), ap, asp, a_quant, hp,
+        _arg(dw, dev, elem, E * n * k, "dw"), int(elem == 2), _arg(dbias, dev, 4, E * n, "dbias"),
+        int(bool(accumulate)), _arg(workspace, dev, ws_elem, 0, "workspace"), ws_bytes, _raw_stream(stream, dev))
+    if code:
+        raise MoeError("moe_expert_grad_weight", code)
+
+
+def moe_combine_backward(cfg: MoeConfig, num_tokens: int, dout: torch.Tensor, y: Optional[torch.Tensor],
+                         topk_w: torch.Tensor, handle: Handle, dy: torch.Tensor, dtopk_w: Optional[torch.Tensor] = None,
+                         stream=None) -> None:
+    """dy[row] = bf16(w[t, k] * dout[t]) and dtopk_w[t, k] = dot(dout[t], y[row]) for every kept pair."""
+    dev, H, P = _device(stream), cfg.hidden, num_tokens * cfg.num_topk
+    rows = moe_rows_capacity(cfg)
+    _arg(handle.pair_to_row, dev, 4, P, "handle")
+    code = _load().moe_combine_backward(
+        ctypes.byref(cfg), num_tokens, _arg(dout, dev, 2, num_tokens * H, "dout"), _arg(y, dev, 2, rows * H, "y"),
+        _arg(topk_w, dev, 4, P, "topk_w"), ctypes.byref(handle.c), _arg(dy, dev, 2, rows * H, "dy"),
+        _arg(dtopk_w, dev, 4, P, "dtopk_w"), _raw_stream(stream, dev))
+    if code:
+        raise MoeError("moe_combine_backward", code)
