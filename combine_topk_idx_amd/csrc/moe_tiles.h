@@ -36,12 +36,12 @@ __device__ __forceinline__ int32_t word_of(const int32_t *a, int32_t i)
 // tile_start[i] = row tiles of BM rows before expert kGroup i, [ceil(E / kGroup)]
 // = all: a table of every expert would not fit beside the stages.  Block-wide,
 // ends with a barrier.
-template <int BM, typename Args>
+template <int BM, int THREADS = kTileThreads, typename Args>
 __device__ inline void scan_tiles(const Args &p, int32_t *tile_start, int32_t *red)
 {
     const int tid = threadIdx.x, lane = tid & (kWave - 1), wave = tid / kWave;
     const int groups = (p.E + kGroup - 1) / kGroup;
-    const int per = (groups + kTileThreads - 1) / kTileThreads;
+    const int per = (groups + THREADS - 1) / THREADS;
     const int e0 = min(groups, tid * per) * kGroup, e1 = min(groups, (tid + 1) * per) * kGroup;
     const auto tiles = [&](int e) {
         return ((e >= p.E ? 0 : p.recv_count != nullptr ? p.recv_count[e] : p.dense_rows) + BM - 1) / BM;
@@ -53,13 +53,13 @@ __device__ inline void scan_tiles(const Args &p, int32_t *tile_start, int32_t *r
     if (lane == kWave - 1)
         red[wave] = incl;
     __syncthreads();
-    int32_t run = dev::sum_before<kTileWaves>(red, wave) + incl - local;
+    int32_t run = dev::sum_before<THREADS / kWave>(red, wave) + incl - local;
     for (int e = e0; e < e1; ++e) {
         if (e % kGroup == 0)
             tile_start[e / kGroup] = run;
         run += tiles(e);
     }
-    if (tid == kTileThreads - 1)
+    if (tid == THREADS - 1)
         tile_start[groups] = run;
     __syncthreads();
 }

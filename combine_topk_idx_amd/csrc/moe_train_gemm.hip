@@ -4,11 +4,11 @@
 //   forward    p[row, j]  = sum over c of a[row, c] w[e, j, c]
 //   gradient   da[row, c] = sum over j of dy[row, j] w[e, j, c]
 //
-// v_mfma_f32_16x16x32_bf16 with the weights as its first operand: a lane's four
-// results belong to one row and four adjacent output channels, and lanes that
-// trade results make whole cache lines of a row.  The gradient sums over the slow
-// axis of the same weights: its stages hold them as they lie in memory, and
-// ds_read_b64_tr_b16 hands each lane four steps of one channel.
+// The weights are the matrix instruction's first operand: a lane's results belong
+// to one row and four output channels, and lanes that trade results make
+// whole cache lines of a row.  The gradient sums over the slow axis of the same
+// weights: its stages hold them as they lie in memory, and transposing reads
+// (ds_read_b64_tr_b16) hand each lane steps of one channel.
 #include "moe_act.h"
 #include "moe_train_tiles.h"
 
@@ -19,28 +19,21 @@ namespace {
 using namespace tile;
 using namespace tile::train;
 
-constexpr int kMGroup = 8;                    // row tiles that walk the channel tiles together
 
 // What is summed over, and the rows' channels.
 template <TrainProduct P>
 __device__ __forceinline__ int32_t depth(const TrainGemmArgs &p) { return P == kGradInput ? p.n : p.k; }
-
-template <int BM>
-struct Stage {
-    static constexpr int kW = BM * kStep * 2;
-    static constexpr int kBytes = kW + kTileN * kStep * 2;
-    static constexpr int kLoads = BM / 64 + 4;  // loads of a wave per step
-};
 
 // The loads of one tile: descriptors (uniform) and this lane's offsets.  Rows
 // past the tile's end are read as its last row and channels past the last as that
 // one (the gradient's: as zeros); what comes of the copies is not stored.  Summed
 // channels past the last are zeros in both operands: bit 31 of an offset takes it
 // past its buffer's end, which the range check turns into zeros.
-template <TrainProduct P, int BM>
+template <TrainProduct P, typename S>
 struct TileLoads {
+    using Rows = RowPlaces<S>;
     __amdgpu_buffer_rsrc_t a, w[2];
-    uint32_t ao[BM / 64], wo[4];
+    uint32_t ao[S::kA], wo[P == kGradInput ? 2 : S::kB];
     const uint16_t *we;  // the gradient's weights
     uint32_t piece;      // first summed channel of this lane's pieces within a step
     int32_t K, wave, stride;
@@ -50,26 +43,20 @@ struct TileLoads {
         wave = wave_;
         K = depth<P>(p);
         const uint32_t row_bytes = (uint32_t)K * 2;
-        // 16-byte piece c of a row sits at position c ^ ((row >> 1) & 7) in LDS:
-        // the 16 rows of a fragment then cover all banks.  A wave loads rows 8 j
-        // .. 8 j + 7, j = wave (mod 8): lane l holds position l % 8 of row l / 8.
-        piece = ((lane & 7) ^ ((4 * (wave & 1) + (lane >> 4)) & 7)) * 8;
-        const int row = 8 * wave + (lane >> 3);
+        const int row = Rows::row(wave, lane);
+        piece = Rows::channel(wave, lane);
         a = buffer(p.rows + at.row0 * K, (uint32_t)at.valid * row_bytes);
 #pragma unroll
-        for (int i = 0; i < BM / 64; ++i)
-            ao[i] = (uint32_t)min(row + 64 * i, at.valid - 1) * row_bytes + piece * 2;
+        for (int i = 0; i < S::kA; ++i)
+            ao[i] = (uint32_t)min(row + Rows::kPass * i, at.valid - 1) * row_bytes + piece * 2;
         if constexpr (P == kGradInput) {
-            // 32 bytes (16 channels) of step s sit at position c ^ (s & 3 | s >> 1 & 4)
-            // of its 512: what 32 lanes read at once then covers all banks.  A wave
-            // loads steps 2 j and 2 j + 1, j = wave (mod 8).
             stride = p.k;
-            const int s = 2 * wave + (lane >> 5);
-            const int f = (s & 3) | ((s >> 1) & 4);
-            const int32_t c = at.nt * kTileN + ((((lane & 31) >> 1) ^ f) * 2 + (lane & 1)) * 8;
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-                wo[i] = c < p.k ? (uint32_t)(s + 16 * i) * (uint32_t)stride * 2 + (uint32_t)c * 2 : 0x80000000u;
+            for (int odd = 0; odd < 2; ++odd) {  // passes by turns
+                const int n = wave + odd * S::kWaves;
+                const int32_t c = at.nt * kTileN + StepPlaces::channel(n, lane);
+                wo[odd] = c < p.k ? (uint32_t)StepPlaces::step(n, lane) * (uint32_t)stride * 2 + (uint32_t)c * 2 : 0x80000000u;
+            }
             we = p.w + (int64_t)at.e * p.n * p.k;
         } else {
 #pragma unroll
@@ -81,8 +68,8 @@ struct TileLoads {
                 w[h] = buffer(p.w + ((int64_t)at.e * p.n + (P == kGated ? h * of : 0) + c) * K,
                               (uint32_t)left * row_bytes);
 #pragma unroll
-                for (int i = 0; i < 2; ++i)
-                    wo[2 * h + i] = (uint32_t)min(row + 64 * i, left - 1) * row_bytes + piece * 2;
+                for (int i = 0; i < S::kB / 2; ++i)
+                    wo[S::kB / 2 * h + i] = (uint32_t)min(row + Rows::kPass * i, left - 1) * row_bytes + piece * 2;
             }
         }
     }
@@ -90,114 +77,87 @@ struct TileLoads {
     template <int FROM, int TO>
     __device__ __forceinline__ void issue(uint8_t *st, int kb) const
     {
-        constexpr int kA = BM / 64;
-        const int32_t k0 = kb * kStep;
+        const int32_t k0 = kb * S::kStep;
         const uint32_t past = (int32_t)piece + k0 < K ? 0u : 0x80000000u;
         const uint32_t at_k = k0 < K ? (uint32_t)k0 * 2 : 0u;
-        __amdgpu_buffer_rsrc_t ws;
-        if constexpr (P == kGradInput && TO > kA)
-            ws = buffer(we + (int64_t)k0 * stride, (uint32_t)max(0, min(kStep, K - k0)) * (uint32_t)stride * 2);
-#pragma unroll
-        for (int j = FROM; j < TO; ++j) {
-            if (j < kA) {
-                load_lds<16>(a, st + (wave + 8 * j) * 1024, ao[j] | past, at_k);
+        for_each<TO - FROM>([&](auto N) {
+            constexpr int j = FROM + decltype(N)::value;
+            if constexpr (j < S::kA) {
+                load_lds<16>(a, st + (wave + S::kWaves * j) * 1024, ao[j] | past, at_k);
             } else {
-                const int i = j - kA;
-                uint8_t *to = st + Stage<BM>::kW + (wave + 8 * i) * 1024;
-                if constexpr (P == kGradInput)
-                    load_lds<16>(ws, to, wo[i], 0);
-                else
-                    load_lds<16>(w[i >> 1], to, wo[i] | past, at_k);
+                constexpr int i = j - S::kA;
+                uint8_t *to = st + S::kW + (wave + S::kWaves * i) * 1024;
+                if constexpr (P == kGradInput) {
+                    const __amdgpu_buffer_rsrc_t ws =
+                        buffer(we + (int64_t)k0 * stride, (uint32_t)max(0, min(S::kStep, K - k0)) * (uint32_t)stride * 2);
+                    load_lds<16>(ws, to, wo[i & 1] + (uint32_t)(i >> 1) * 4 * S::kWaves * (uint32_t)stride * 2, 0);
+                } else {
+                    load_lds<16>(w[i / (S::kB / 2)], to, wo[i] | past, at_k);
+                }
             }
-        }
+        });
     }
 };
 
-// acc += the stage's step for this wave's MT row fragments and kNF channel
-// fragments, while step `kb_load` loads into the stage `free`: its loads are
-// spread over the matrix instructions.
-template <TrainProduct P, int BM, int MT>
-__device__ __forceinline__ void multiply_stage(dev::f32x4 (&acc)[kNF][MT], const uint8_t *st, int wr, int wc, int lane,
-                                               const TileLoads<P, BM> &loads, uint8_t *free, int kb_load)
-{
-    constexpr int kLoads = Stage<BM>::kLoads;
-    const int r = lane & 15, g = lane >> 4;
-    const int rswz = (r >> 1) & 7;
-    const int rlo = r * 128 + ((g ^ rswz) * 16), rhi = r * 128 + (((4 + g) ^ rswz) * 16);
-    const uint8_t *rows = st + wr * MT * 16 * 128;
-    const uint8_t *ws = st + Stage<BM>::kW;
-    const int column = (8 * g + (r >> 2)) * 2 * kTileN + ((r >> 2) | (g & 1) << 2) * 32 + (r & 3) * 8;
-    Fragment w[kNF], x[2];
-#pragma unroll
-    for (int f = 0; f < kNF; ++f) {
-        if constexpr (P == kGradInput) {
-            w[f] = read_columns<kTileN>(ws + (column ^ (wc * 4 + f) * 32));
-        } else {
-            const int c = P == kGated ? wc * 32 + (f & 1) * 16 + (f >> 1) * 128 : wc * 64 + f * 16;
-            w[f] = read_rows(ws + c * 128, rlo, rhi);
-        }
-        if (f == 0)
-            x[0] = read_rows(rows, rlo, rhi);
+// Where a lane finds its fragments in a stage.
+template <TrainProduct P, typename S, int MT>
+struct TileReads {
+    int row, column, rows, channels;
+
+    __device__ __forceinline__ TileReads(int wave, int lane)
+    {
+        row = RowPlaces<S>::read(lane);
+        rows = wave / S::WC * MT * 16 * S::kRow;
+        channels = wave % S::WC;
+        column = StepPlaces::read(lane);
     }
-    const auto part = [&](auto I) {
-        constexpr int i = decltype(I)::value;
-        if constexpr (i + 1 < MT)
-            x[(i + 1) & 1] = read_rows(rows + (i + 1) * 16 * 128, rlo, rhi);
-#pragma unroll
-        for (int h = 0; h < 2; ++h)
-#pragma unroll
-            for (int f = 0; f < kNF; ++f)
-                acc[f][i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w[f].h[h], x[i & 1].h[h], acc[f][i], 0, 0, 0);
-        loads.template issue<i * kLoads / MT, (i + 1) * kLoads / MT>(free, kb_load);
-        __builtin_amdgcn_sched_barrier(0);
-    };
-    for_each<MT>(part);
-}
+    // 16 rows, or 16 channels, of half h of a step.
+    __device__ __forceinline__ dev::bf16x8 x(const uint8_t *st, int i, int h) const
+    {
+        return *reinterpret_cast<const dev::bf16x8 *>(st + rows + i * 16 * S::kRow + (row ^ h * 64));
+    }
+    __device__ __forceinline__ dev::bf16x8 w(const uint8_t *st, int f, int h) const
+    {
+        if constexpr (P == kGradInput)
+            return read_steps(st + S::kW + (column ^ (channels * S::NF + f) * 32) + h * 64 * kTileN);
+        // gated: the first half of a wave's fragments are gate channels
+        constexpr int kHalf = S::NF / 2;
+        const int c = P == kGated ? (channels * kHalf + f % kHalf) * 16 + f / kHalf * 128 : (channels * S::NF + f) * 16;
+        return *reinterpret_cast<const dev::bf16x8 *>(st + S::kW + c * S::kRow + (row ^ h * 64));
+    }
+};
 
 // ---- results ----------------------------------------------------------------------
 
-// The rows' bf16 that store_lines would overwrite, as fragments of fp32.
-__device__ __forceinline__ void load_lines(__amdgpu_buffer_rsrc_t in, dev::f32x4 (&v)[kNF], int row0, int valid,
-                                           int32_t c0, int32_t channels, int lane)
+// How the waves of a tile share the 128-channel blocks of saved rows in 8 bits: a
+// block is that of one to four waves; an MXFP8 block is a pair of fragments.
+template <TrainProduct P, typename S>
+struct SavedBlocks {
+    static constexpr int kHalves = P == kGated ? 2 : 1;       // gate and up, or all channels
+    static constexpr int kOwn = S::NF / kHalves;              // fragments of a half, per wave
+    static constexpr int kShare = kQuantGroup / (kOwn * 16);  // waves of a block
+};
+
+// Largest magnitude of a row's channels in COUNT fragments of a wave.
+template <int COUNT>
+__device__ __forceinline__ float largest(const dev::f32x4 *v)
 {
-    const int r = lane & 15, g = lane >> 4;
-    const bool low = r < 8;
-    const int32_t c = c0 + (low ? 0 : 32) + (g & 1) * 16 + (g >> 1) * 8;
-    dev::u32x4 s[2];
+    float m = 0.0f;
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-        const int row = row0 + h * 8 + (r & 7);
-        const uint32_t off = row < valid && c < channels ? ((uint32_t)row * (uint32_t)channels + c) * 2 : 0x80000000u;
-        s[h] = __builtin_amdgcn_raw_buffer_load_b128(in, off, 0, 0);
-    }
-    trade_rows(s, low);
-    trade_fragments(s[0]);
-    trade_fragments(s[1]);
+    for (int f = 0; f < COUNT; ++f)
 #pragma unroll
-    for (int f = 0; f < kNF; ++f) {
-        const uint32_t lo = s[f >> 1][(f & 1) * 2], hi = s[f >> 1][(f & 1) * 2 + 1];
-        v[f] = dev::f32x4{dev::bf16_lo(lo), dev::bf16_hi(lo), dev::bf16_lo(hi), dev::bf16_hi(hi)};
-    }
+        for (int j = 0; j < 4; ++j)
+            m = fmaxf(m, fabsf(v[f][j]));
+    m = fmaxf(m, __shfl_xor(m, 16));
+    return fmaxf(m, __shfl_xor(m, 32));
 }
 
-// One pair of fragments -- 32 adjacent channels from c0 of 16 rows -- as bf16.
-__device__ __forceinline__ void store_pair(__amdgpu_buffer_rsrc_t out, const dev::f32x4 &a, const dev::f32x4 &b, int row,
-                                           int valid, int32_t c0, bool inside, int32_t channels, int g)
+// One row fragment's saved rows in 8 bits.
+template <TrainProduct P, int QUANT, typename S>
+__device__ __forceinline__ void save_quantized(const TrainGemmArgs &p, const dev::f32x4 (&v)[S::NF], const TileAt &at,
+                                               int row0, int wc, int lane, const float (*wave_max)[S::WC][S::BM])
 {
-    dev::u32x4 s = pack_fragments(a, b);
-    trade_fragments(s);
-    const int32_t c = c0 + (g & 1) * 16 + (g >> 1) * 8;
-    const uint32_t off = row < valid && inside ? ((uint32_t)row * (uint32_t)channels + c) * 2 : 0x80000000u;
-    __builtin_amdgcn_raw_buffer_store_b128(s, out, off, 0, kStreamed);
-}
-
-// Saved rows in 8 bits.  A 128-channel block is that of two waves (of four in
-// each of the gated block's halves); an MXFP8 block is a pair of fragments.
-template <TrainProduct P, int QUANT, int MT, int BM>
-__device__ __forceinline__ void save_quantized(const TrainGemmArgs &p, const dev::f32x4 (&acc)[kNF][MT], const TileAt &at,
-                                               int wr, int wc, int lane, float (*wave_max)[kWaveCols][BM])
-{
-    const int r = lane & 15, g = lane >> 4;
+    using B = SavedBlocks<P, S>;
     const int32_t half = P == kGated ? p.n / 2 : p.n;
     constexpr int kScale = QUANT == MOE_QUANT_FP8_UE8M0 ? 1 : 4;  // bytes of 128 channels' scales
     const int32_t NB = p.n / kQuantGroup, row_scale = (NB * kScale + 3) / 4 * 4;
@@ -205,63 +165,40 @@ __device__ __forceinline__ void save_quantized(const TrainGemmArgs &p, const dev
         buffer(static_cast<uint8_t *>(p.saved) + at.row0 * p.n, (uint32_t)at.valid * (uint32_t)p.n);
     const __amdgpu_buffer_rsrc_t scales =
         buffer(static_cast<uint8_t *>(p.saved_scale) + at.row0 * row_scale, (uint32_t)at.valid * (uint32_t)row_scale);
-    const auto largest = [&](int i, int h) {  // of this wave's 32 channels of its row
+    const int g = lane >> 4, row = row0 + (lane & 15);
+#pragma unroll
+    for (int h = 0; h < B::kHalves; ++h) {
         float m = 0.0f;
+        if constexpr (QUANT != MOE_QUANT_MXFP8 && B::kShare == 1)
+            m = largest<B::kOwn>(&v[h * B::kOwn]);
+        if constexpr (QUANT != MOE_QUANT_MXFP8 && B::kShare > 1) {
 #pragma unroll
-        for (int f = 2 * h; f < 2 * h + 2; ++f)
+            for (int u = 0; u < B::kShare; ++u)
+                m = fmaxf(m, wave_max[h][wc / B::kShare * B::kShare + u][row]);
+        }
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
-                m = fmaxf(m, fabsf(acc[f][i][j]));
-        m = fmaxf(m, __shfl_xor(m, 16));
-        return fmaxf(m, __shfl_xor(m, 32));
-    };
-    if constexpr (QUANT != MOE_QUANT_MXFP8) {
-#pragma unroll
-        for (int i = 0; i < MT; ++i)
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const float m = largest(i, h);
-                if (g == 0)
-                    wave_max[h][wc][(wr * MT + i) * 16 + r] = m;
-            }
-        meet();
-    }
-#pragma unroll
-    for (int i = 0; i < MT; ++i) {
-        const int row = (wr * MT + i) * 16 + r;
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            // gated: pair h is the gate's or the up product's; else 32 of 64 channels
-            const int32_t c = P == kGated ? at.nt * 128 + wc * 32 : at.nt * kTileN + wc * 64 + h * 32;
+        for (int f = 0; f < B::kOwn; f += 2) {
+            const int32_t c = at.nt * (kTileN / B::kHalves) + (wc * B::kOwn + f) * 16;
             const bool inside = row < at.valid && c < half;
-            const int32_t channel = c + (P == kGated ? h * half : 0);
-            float m;
-            if constexpr (QUANT == MOE_QUANT_MXFP8) {
-                m = largest(i, h);
-            } else if constexpr (P == kGated) {
-                m = fmaxf(fmaxf(wave_max[h][0][row], wave_max[h][1][row]),
-                          fmaxf(wave_max[h][2][row], wave_max[h][3][row]));
-            } else {
-                m = fmaxf(fmaxf(wave_max[0][wc][row], wave_max[1][wc][row]),
-                          fmaxf(wave_max[0][wc ^ 1][row], wave_max[1][wc ^ 1][row]));
-            }
+            const int32_t channel = c + h * half;
+            const dev::f32x4 *of = &v[h * B::kOwn + f];
+            if constexpr (QUANT == MOE_QUANT_MXFP8)
+                m = largest<2>(of);
             const dev::BlockScale<QUANT> bs(m);
-            uint32_t q[2];
+            uint32_t e4m3[2];
 #pragma unroll
-            for (int f = 0; f < 2; ++f) {
-                const dev::f32x4 &v = acc[2 * h + f][i];
-                q[f] = dev::pack_e4m3(bs.apply(v[0]), bs.apply(v[1]), bs.apply(v[2]), bs.apply(v[3]));
-            }
-            const auto pair = __builtin_amdgcn_permlane16_swap(q[0], q[1], false, false);
+            for (int u = 0; u < 2; ++u)
+                e4m3[u] = dev::pack_e4m3(bs.apply(of[u][0]), bs.apply(of[u][1]), bs.apply(of[u][2]), bs.apply(of[u][3]));
+            const auto pair = __builtin_amdgcn_permlane16_swap(e4m3[0], e4m3[1], false, false);
             const uint32_t off = (uint32_t)row * (uint32_t)p.n + channel + (g & 1) * 16 + (g >> 1) * 8;
             __builtin_amdgcn_raw_buffer_store_b64(dev::u32x2{pair[0], pair[1]}, out, inside ? off : 0x80000000u, 0, 0);
             if constexpr (QUANT == MOE_QUANT_MXFP8) {
                 const uint32_t soff = (uint32_t)row * row_scale + channel / 32;
                 __builtin_amdgcn_raw_buffer_store_b8((uint8_t)bs.byte, scales, inside && g == 0 ? soff : 0x80000000u, 0, 0);
-            } else {
+            } else if (f == 0) {
                 const int32_t b = channel / kQuantGroup;
-                const bool first = P == kGated ? wc == 0 : h == 0 && (wc & 1) == 0;
-                const uint32_t soff = inside && g == 0 && first ? (uint32_t)row * row_scale + b * kScale : 0x80000000u;
+                const bool one = inside && g == 0 && wc % B::kShare == 0;
+                const uint32_t soff = one ? (uint32_t)row * row_scale + b * kScale : 0x80000000u;
                 if constexpr (QUANT == MOE_QUANT_FP8_F32) {
                     __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(bs.s), scales, soff, 0, 0);
                 } else {
@@ -275,180 +212,217 @@ __device__ __forceinline__ void save_quantized(const TrainGemmArgs &p, const dev
     }
 }
 
-// Writes a wave's results: rows 16 (MT wr + i) + (lane % 16), channels 4 (lane /
-// 16) + j of fragment f.
-template <TrainProduct P, int MT, int BM>
-__device__ __forceinline__ void write_tile(const TrainGemmArgs &p, dev::f32x4 (&acc)[kNF][MT], const TileAt &at, int wr,
-                                           int wc, int lane, float (*wave_max)[kWaveCols][BM])
+// COUNT adjacent fragments of one row fragment.
+template <int COUNT>
+__device__ __forceinline__ void store_fragments(const Lines &to, const dev::f32x4 *v, int row0, int32_t c0, int lane)
 {
-    const int r = lane & 15, g = lane >> 4;
-    if constexpr (P == kGradInput) {
-        const __amdgpu_buffer_rsrc_t out = buffer(p.y + at.row0 * p.k, (uint32_t)at.valid * (uint32_t)p.k * 2);
+    if constexpr (COUNT == 2) {
+        store_pair(to, v[0], v[1], row0, c0, lane);
+    } else {
 #pragma unroll
-        for (int i = 0; i < MT; ++i) {
-            const dev::f32x4 v[kNF] = {acc[0][i], acc[1][i], acc[2][i], acc[3][i]};
-            store_lines(out, v, (wr * MT + i) * 16, at.valid, at.nt * kTileN + wc * 64, p.k, lane);
-        }
-        return;
+        for (int f = 0; f < COUNT; f += 4)
+            store_lines(to, v[f], v[f + 1], v[f + 2], v[f + 3], row0, c0 + f * 16, lane);
     }
-    const int32_t c0 = at.nt * kTileN + wc * 64;
-    if (P == kLinear && p.bias != nullptr) {
-        const __amdgpu_buffer_rsrc_t bias = buffer(p.bias + (int64_t)at.e * p.n, (uint32_t)p.n * 2);
+}
+
+// Writes a wave's results, one row fragment at a time, from the sums into other
+// registers: sums that an epilogue changes would leave the accumulators.
+template <TrainProduct P, typename S, int MT>
+__device__ __forceinline__ void write_tile(const TrainGemmArgs &p, const dev::f32x4 (&acc)[S::NF][MT], const TileAt &at,
+                                           int wr, int wc, int lane, float (*wave_max)[S::WC][S::BM])
+{
+    constexpr int NF = S::NF;
+    using B = SavedBlocks<P, S>;
+    const int g = lane >> 4;
+    const int32_t channels = P == kGated ? p.n / 2 : P == kGradInput ? p.k : p.n;
+    // this wave's channels (gated: of a half)
+    const int32_t c0 = P == kGated ? at.nt * 128 + wc * (NF / 2) * 16 : at.nt * kTileN + wc * NF * 16;
+    const uint32_t bytes = (uint32_t)at.valid * (uint32_t)channels * 2;
+    const Lines out = {buffer(p.y + at.row0 * channels, bytes), at.valid, channels, 0, channels};
+    Lines saved, residual;
+    dev::f32x4 add[NF];
+    if constexpr (P != kGradInput)
+        saved = Lines{buffer(p.saved != nullptr ? static_cast<uint16_t *>(p.saved) + at.row0 * p.n : p.y,
+                             (uint32_t)at.valid * (uint32_t)p.n * 2),
+                      at.valid, channels, 0, p.n};
+    if constexpr (P == kLinear) {
+        residual = Lines{buffer(p.residual != nullptr ? p.residual + at.row0 * channels : p.y, bytes), at.valid, channels, 0,
+                         channels};
+        const __amdgpu_buffer_rsrc_t bias =
+            buffer(p.bias != nullptr ? p.bias + (int64_t)at.e * p.n : p.y, p.bias != nullptr ? (uint32_t)p.n * 2 : 0);
 #pragma unroll
-        for (int f = 0; f < kNF; ++f) {
+        for (int f = 0; f < NF; ++f) {  // zeros past the buffer's end
             const dev::u32x2 b = __builtin_amdgcn_raw_buffer_load_b64(bias, (uint32_t)(c0 + f * 16 + 4 * g) * 2, 0, 0);
-            const dev::f32x4 add = {dev::bf16_lo(b[0]), dev::bf16_hi(b[0]), dev::bf16_lo(b[1]), dev::bf16_hi(b[1])};
-#pragma unroll
-            for (int i = 0; i < MT; ++i)
-                acc[f][i] += add;
+            add[f] = dev::f32x4{dev::bf16_lo(b[0]), dev::bf16_hi(b[0]), dev::bf16_lo(b[1]), dev::bf16_hi(b[1])};
         }
     }
-    if (p.saved != nullptr) {
-        if (p.saved_quant == MOE_QUANT_FP8_F32) {
-            save_quantized<P, MOE_QUANT_FP8_F32, MT, BM>(p, acc, at, wr, wc, lane, wave_max);
-        } else if (p.saved_quant == MOE_QUANT_FP8_UE8M0) {
-            save_quantized<P, MOE_QUANT_FP8_UE8M0, MT, BM>(p, acc, at, wr, wc, lane, wave_max);
-        } else if (p.saved_quant == MOE_QUANT_MXFP8) {
-            save_quantized<P, MOE_QUANT_MXFP8, MT, BM>(p, acc, at, wr, wc, lane, wave_max);
-        } else {
-            const __amdgpu_buffer_rsrc_t out = buffer(static_cast<uint16_t *>(p.saved) + at.row0 * p.n,
-                                                      (uint32_t)at.valid * (uint32_t)p.n * 2);
+    const auto row_sums = [&](auto I, dev::f32x4 (&v)[NF]) {
+        constexpr int i = decltype(I)::value;
+        for_each<NF>([&](auto F) {
+            constexpr int f = decltype(F)::value;
+            v[f] = acc[f][i];
+            if constexpr (P == kLinear)
+                v[f] += add[f];
+        });
+    };
+    const bool quantized = P != kGradInput && p.saved != nullptr && p.saved_quant != MOE_QUANT_NONE;
+    if constexpr (P != kGradInput && B::kShare > 1) {
+        if (quantized && p.saved_quant != MOE_QUANT_MXFP8) {
+            for_each<MT>([&](auto I) {
+                dev::f32x4 v[NF];
+                row_sums(I, v);
 #pragma unroll
-            for (int i = 0; i < MT; ++i) {
-                const int row = (wr * MT + i) * 16;
+                for (int h = 0; h < B::kHalves; ++h) {
+                    const float m = largest<B::kOwn>(&v[h * B::kOwn]);
+                    if (g == 0)
+                        wave_max[h][wc][(wr * MT + decltype(I)::value) * 16 + lane] = m;
+                }
+                __builtin_amdgcn_sched_barrier(0);
+            });
+            meet();
+        }
+    }
+    for_each<MT>([&](auto I) {
+        const int row0 = (wr * MT + decltype(I)::value) * 16;
+        dev::f32x4 v[NF];
+        row_sums(I, v);
+        if constexpr (P != kGradInput) {
+            if (quantized) {
+                if (p.saved_quant == MOE_QUANT_FP8_F32)
+                    save_quantized<P, MOE_QUANT_FP8_F32, S>(p, v, at, row0, wc, lane, wave_max);
+                else if (p.saved_quant == MOE_QUANT_FP8_UE8M0)
+                    save_quantized<P, MOE_QUANT_FP8_UE8M0, S>(p, v, at, row0, wc, lane, wave_max);
+                else
+                    save_quantized<P, MOE_QUANT_MXFP8, S>(p, v, at, row0, wc, lane, wave_max);
+            } else if (p.saved != nullptr) {
+                store_fragments<B::kOwn>(saved, v, row0, c0, lane);
                 if constexpr (P == kGated) {
-                    const int32_t c = at.nt * 128 + wc * 32, half = p.n / 2;
-                    const bool inside = c + (g & 1) * 16 + (g >> 1) * 8 < half;
-                    store_pair(out, acc[0][i], acc[1][i], row + r, at.valid, c, inside, p.n, g);
-                    store_pair(out, acc[2][i], acc[3][i], row + r, at.valid, c + half, inside, p.n, g);
-                } else {
-                    const dev::f32x4 v[kNF] = {acc[0][i], acc[1][i], acc[2][i], acc[3][i]};
-                    store_lines(out, v, row, at.valid, c0, p.n, lane);
+                    Lines up = saved;
+                    up.shift = channels;
+                    store_fragments<B::kOwn>(up, v + B::kOwn, row0, c0, lane);
                 }
             }
         }
-    }
-    if constexpr (P == kGated) {
-        const int32_t inter = p.n / 2;
-        const __amdgpu_buffer_rsrc_t out = buffer(p.y + at.row0 * inter, (uint32_t)at.valid * (uint32_t)inter * 2);
-        const int32_t c = at.nt * 128 + wc * 32;
-        const bool inside = c + (g & 1) * 16 + (g >> 1) * 8 < inter;
+        if constexpr (P == kGated)
+            dev::for_act(p.act, [&](auto act) {
 #pragma unroll
-        for (int i = 0; i < MT; ++i) {
+                for (int f = 0; f < NF / 2; ++f)
 #pragma unroll
-            for (int f = 0; f < 2; ++f)
+                    for (int j = 0; j < 4; ++j)
+                        v[f][j] = dev::act_value<decltype(act)::value>(v[f][j]) * v[f + NF / 2][j];
+            });
+        if constexpr (P == kLinear) {
+            if (p.act != MOE_ACT_NONE)
+                dev::for_act(p.act, [&](auto act) {
 #pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    acc[f][i][j] = dev::act_value(p.act, acc[f][i][j]) * acc[f + 2][i][j];
-            store_pair(out, acc[0][i], acc[1][i], (wr * MT + i) * 16 + r, at.valid, c, inside, inter, g);
-        }
-    } else if constexpr (P == kLinear) {
-        const uint32_t bytes = (uint32_t)at.valid * (uint32_t)p.n * 2;
-        const __amdgpu_buffer_rsrc_t out = buffer(p.y + at.row0 * p.n, bytes);
-        const bool add = p.residual != nullptr;
-        const __amdgpu_buffer_rsrc_t residual = buffer(add ? p.residual + at.row0 * p.n : p.y, add ? bytes : 0);
+                    for (int f = 0; f < NF; ++f)
 #pragma unroll
-        for (int i = 0; i < MT; ++i) {
-            const int row = (wr * MT + i) * 16;
-            dev::f32x4 v[kNF];
+                        for (int j = 0; j < 4; ++j)
+                            v[f][j] = dev::act_value<decltype(act)::value>(v[f][j]);
+                });
+            if (p.residual != nullptr) {
 #pragma unroll
-            for (int f = 0; f < kNF; ++f)
-#pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    v[f][j] = dev::act_value(p.act, acc[f][i][j]);
-            if (add) {
-                dev::f32x4 res[kNF];
-                load_lines(residual, res, row, at.valid, c0, p.n, lane);
-#pragma unroll
-                for (int f = 0; f < kNF; ++f)
-                    v[f] += res[f];
+                for (int f = 0; f < NF; f += 4)
+                    add_lines(residual, &v[f], row0, c0 + f * 16, lane);
             }
-            store_lines(out, v, row, at.valid, c0, p.n, lane);
         }
-    }
+        store_fragments<P == kGated ? NF / 2 : NF>(out, v, row0, c0, lane);
+        __builtin_amdgcn_sched_barrier(0);  // one row fragment's registers at a time
+    });
 }
 
-// Starts the loads of a tile's first NS - 1 stages.
-template <TrainProduct P, int BM, int NS>
-__device__ __forceinline__ void start_tile(const TrainGemmArgs &p, const TileAt &at, uint8_t *st0, uint8_t *st1, int wave,
-                                           int lane)
+// 128 rows: eight waves, two per SIMD, three stages of which two are in flight.
+using Rows128 = TileShape<128, 2, 4, 64, 3>;
+// 256 rows: four waves, one per SIMD, each with 128 x 128: the LDS reads of a
+// matrix instruction fall to two thirds of what eight waves of 128 x 64 need, which
+// together with the loads' writes would keep LDS as busy as the matrix cores.
+using Rows256 = TileShape<256, 2, 2, 64, 2>;
+
+// Starts the loads of a tile's first two stages.
+template <TrainProduct P, typename S>
+__device__ __forceinline__ void start_tile(const TrainGemmArgs &p, const TileAt &at, const Stages &st, int wave, int lane)
 {
-    TileLoads<P, BM> loads;
+    TileLoads<P, S> loads;
     loads.set(p, at, wave, lane);
-    loads.template issue<0, Stage<BM>::kLoads>(st0, 0);
+    loads.template issue<0, S::kLoads>(st.s0, 0);
     __builtin_amdgcn_sched_barrier(0);  // in this order: the waits count
-    if constexpr (NS == 3)
-        loads.template issue<0, Stage<BM>::kLoads>(st1, 1);
+    loads.template issue<0, S::kLoads>(st.s1, 1);
     __builtin_amdgcn_sched_barrier(0);
 }
 
-// Multiplies a tile whose first NS - 1 stages are in flight, then starts the
-// next tile's (`more`) and writes the results.
-template <TrainProduct P, int BM, int NS, int MT>
+// Multiplies a tile whose first two stages are in flight, then starts the next
+// tile's (`more`) and writes the results.
+template <TrainProduct P, typename S, int MT>
 __device__ __forceinline__ void run_tile(const TrainGemmArgs &p, const TileAt &at, const TileAt &next, bool more,
-                                         uint8_t *st0, uint8_t *st1, uint8_t *st2, float (*wave_max)[kWaveCols][BM],
-                                         int wave, int lane)
+                                         const Stages &st, float (*wave_max)[S::WC][S::BM], int wave, int lane)
 {
-    TileLoads<P, BM> loads;
+    TileLoads<P, S> loads;
     loads.set(p, at, wave, lane);
-    constexpr int kAhead = Stage<BM>::kLoads * (NS - 2);
-    const int wr = wave / kWaveCols, wc = wave % kWaveCols;
-    const int KB = (loads.K + kStep - 1) / kStep;
-    dev::f32x4 acc[kNF][MT];
-#pragma unroll
-    for (int f = 0; f < kNF; ++f)
-#pragma unroll
-        for (int i = 0; i < MT; ++i)
-            acc[f][i] = dev::f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-    const auto step = [&](uint8_t *cur, uint8_t *free, int kb) {
-        wait_and_meet<kAhead>();
-        multiply_stage<P, BM, MT>(acc, cur, wr, wc, lane, loads, free, kb + NS - 1);
-    };
-    // The first steps stand before the loop: there the compiler's own waits allow
-    // for the stores of the tile before, in the loop they would hold up each turn.
-    step(st0, NS == 3 ? st2 : st1, 0);
-    if constexpr (NS == 3) {
+    const TileReads<P, S, MT> reads(wave, lane);
+    const int KB = scalar((loads.K + S::kStep - 1) / S::kStep);
+    dev::f32x4 acc[S::NF][MT];
+    clear(acc);
+    if constexpr (S::kStages == 3) {
+        const auto step = [&](uint8_t *cur, uint8_t *free, int kb) {
+            wait_and_meet<S::kLoads>();
+            multiply_stage<S, MT>(acc, cur, reads, loads, free, kb + 2);
+        };
+        // The first steps stand before the loop: there the compiler's own waits allow
+        // for the stores of the tile before, in the loop they would hold up each turn.
+        step(st.s0, st.s2, 0);
         if (KB > 1) {
-            step(st1, st0, 1);
+            step(st.s1, st.s0, 1);
             int kb = 2;
             for (; kb + 3 <= KB; kb += 3) {
-                step(st2, st1, kb);
-                step(st0, st2, kb + 1);
-                step(st1, st0, kb + 2);
+                step(st.s2, st.s1, kb);
+                step(st.s0, st.s2, kb + 1);
+                step(st.s1, st.s0, kb + 2);
             }
             if (kb < KB)
-                step(st2, st1, kb);
+                step(st.s2, st.s1, kb);
             if (kb + 1 < KB)
-                step(st0, st2, kb + 1);
+                step(st.s0, st.s2, kb + 1);
         }
     } else {
-        int kb = 1;
-        for (; kb + 2 <= KB; kb += 2) {
-            step(st1, st0, kb);
-            step(st0, st1, kb + 1);
+        // Half a step is read while the half before is multiplied.  Between a step's
+        // halves the waves meet: the next stage is there and this one has been read, so
+        // the step after next loads into it.
+        Fragments<S, MT> first, second;
+        const auto none = [](auto, const dev::bf16x8 &) {};
+        const auto step = [&](uint8_t *cur, uint8_t *other, int kb) {
+            multiply<false, S, MT>(acc, first, second, cur, 1, reads, loads, cur, 0, none);
+            wait_and_meet<0>();
+            multiply<true, S, MT>(acc, second, first, other, 0, reads, loads, cur, kb + 2, none);
+        };
+        wait_and_meet<S::kLoads>();
+        for_each<MT + S::NF>([&](auto N) { read_fragment<decltype(N)::value, S, MT>(first, st.s0, 0, reads); });
+        // Whole pairs: a step past the last multiplies zeros.  With a remainder of its own
+        // the sums would change registers where the ways meet.
+        for (int kb = 0; kb < KB; kb += 2) {
+            step(st.s0, st.s1, kb);
+            step(st.s1, st.s0, kb + 1);
+            end_turn(kb + 2, KB);
         }
-        if (kb < KB)
-            step(st1, st0, kb);
     }
     wait_and_meet<0>();
     if (more)
-        start_tile<P, BM, NS>(p, next.scalars(), st0, st1, wave, lane);
-    write_tile<P, MT, BM>(p, acc, at, wr, wc, lane, wave_max);
+        start_tile<P, S>(p, next.scalars(), st, wave, lane);
+    write_tile<P, S, MT>(p, acc, at, wave / S::WC, wave % S::WC, lane, wave_max);
 }
 
-template <TrainProduct P, int BM, int NS>
-__global__ __launch_bounds__(kTileThreads) void train_gemm_tiles(TrainGemmArgs p, int32_t n_tiles)
+template <TrainProduct P, typename S>
+__global__ __launch_bounds__(S::kThreads, 1) void train_gemm_tiles(TrainGemmArgs p, int32_t n_tiles)
 {
+    constexpr int BM = S::BM;
     __shared__ int32_t tile_start[kMaxExperts / kGroup + 1];
-    __shared__ int32_t red[kTileWaves];
-    // separate variables: the compiler then knows which reads follow which loads
-    __shared__ alignas(1024) uint8_t st0[Stage<BM>::kBytes];
-    __shared__ alignas(1024) uint8_t st1[Stage<BM>::kBytes];
-    __shared__ alignas(1024) uint8_t st2[NS == 3 ? Stage<BM>::kBytes : 16];
-    __shared__ float wave_max[P == kGradInput ? 1 : 2][kWaveCols][BM];
+    __shared__ int32_t red[S::kWaves];
+    __shared__ alignas(1024) uint8_t st0[S::kBytes], st1[S::kBytes];
+    __shared__ alignas(1024) uint8_t st2[S::kStages == 3 ? S::kBytes : 16];
+    const Stages st = {st0, st1, st2, nullptr};
+    __shared__ float wave_max[P == kGated ? 2 : 1][S::WC][BM];
     const int lane = threadIdx.x & (kWave - 1);
     const int wave = scalar(threadIdx.x / kWave);
-    scan_tiles<BM>(p, tile_start, red);
+    scan_tiles<BM, S::kThreads>(p, tile_start, red);
     const int64_t n_work = (int64_t)scalar(tile_start[(p.E + kGroup - 1) / kGroup]) * n_tiles;
     // workgroups go to the 8 XCDs in turn: each XCD takes a contiguous run of
     // the work, so that the tiles of one expert share its L2
@@ -456,18 +430,19 @@ __global__ __launch_bounds__(kTileThreads) void train_gemm_tiles(TrainGemmArgs p
     const int64_t base = (int64_t)(blockIdx.x & 7) * run;
     const int64_t end = min(run, n_work - base);
 
-    // tiles of an expert: groups of kMGroup row tiles; inside a group the row
-    // tiles of one channel tile are adjacent (they share its weights)
+    // tiles of an expert: groups of 3 to 5 row tiles, alike in size; inside a group
+    // the row tiles of one channel tile are adjacent (they share its weights)
     const auto locate = [&](int32_t m, int32_t rem) {  // number m * n_tiles + rem
         TileAt at;
         const ExpertAt ex = find_expert<BM>(p, tile_start, m);
         const int32_t e_tiles = (ex.rows + BM - 1) / BM;
-        const int32_t grp = (m - ex.start) / kMGroup;
-        const int32_t in_grp = (m - ex.start) % kMGroup * n_tiles + rem;
-        const int32_t grp_rows = min(kMGroup, e_tiles - grp * kMGroup);
+        const int32_t groups = max(1, (e_tiles + 2) / 4), size = (e_tiles + groups - 1) / groups;
+        const int32_t grp = (m - ex.start) / size;
+        const int32_t in_grp = (m - ex.start) % size * n_tiles + rem;
+        const int32_t grp_rows = min(size, e_tiles - grp * size);
         at.e = scalar(ex.e);
         at.nt = scalar(in_grp / grp_rows);
-        const int32_t first = scalar((grp * kMGroup + in_grp % grp_rows) * BM);
+        const int32_t first = scalar((grp * size + in_grp % grp_rows) * BM);
         at.valid = scalar(min(BM, ex.rows - first));
         at.row0 = (int64_t)(p.expert_offset != nullptr ? word_of(p.expert_offset, at.e) : 0) + first;
         return at;
@@ -479,7 +454,7 @@ __global__ __launch_bounds__(kTileThreads) void train_gemm_tiles(TrainGemmArgs p
     int32_t rem = scalar((int32_t)((base + idx) - (int64_t)m * n_tiles));
     const int32_t m_step = scalar((gridDim.x >> 3) / n_tiles), rem_step = (gridDim.x >> 3) - m_step * n_tiles;
     TileAt next = locate(m, rem);
-    start_tile<P, BM, NS>(p, next, st0, st1, wave, lane);
+    start_tile<P, S>(p, next, st, wave, lane);
     for (;;) {
         const TileAt at = next.scalars();
         idx += gridDim.x >> 3;
@@ -493,13 +468,13 @@ __global__ __launch_bounds__(kTileThreads) void train_gemm_tiles(TrainGemmArgs p
         if (more)
             next = locate(m, rem);
         // a tile that is not full takes the code for its size
-        constexpr int MT = BM / 16 / kWaveRows, M2 = (MT + 1) / 2, M1 = (MT + 3) / 4;
-        if (at.valid > M2 * 32)
-            run_tile<P, BM, NS, MT>(p, at, next, more, st0, st1, st2, wave_max, wave, lane);
-        else if (at.valid > M1 * 32)
-            run_tile<P, BM, NS, M2>(p, at, next, more, st0, st1, st2, wave_max, wave, lane);
+        constexpr int MT = S::MT, kWide = 16 * S::WR;
+        if (at.valid > MT / 2 * kWide)
+            run_tile<P, S, MT>(p, at, next, more, st, wave_max, wave, lane);
+        else if (at.valid > MT / 4 * kWide)
+            run_tile<P, S, MT / 2>(p, at, next, more, st, wave_max, wave, lane);
         else
-            run_tile<P, BM, NS, M1>(p, at, next, more, st0, st1, st2, wave_max, wave, lane);
+            run_tile<P, S, MT / 4>(p, at, next, more, st, wave_max, wave, lane);
         if (!more)
             break;
     }
@@ -513,17 +488,17 @@ int64_t max_tiles(const TrainGemmArgs &p, int32_t rows)
     return p.max_rows / rows + (p.max_rows < p.E ? p.max_rows : p.E);
 }
 
-template <TrainProduct P, int BM, int NS>
+template <TrainProduct P, typename S>
 hipError_t launch_tiles(const TrainGemmArgs &p, hipStream_t stream)
 {
     const int32_t channels = P == kGated ? p.n / 2 : P == kGradInput ? p.k : p.n;
     const int32_t width = P == kGated ? kTileN / 2 : kTileN;
     const int32_t n_tiles = (channels + width - 1) / width;
-    const int64_t tiles = max_tiles(p, BM) * n_tiles;
+    const int64_t tiles = max_tiles(p, S::BM) * n_tiles;
     // one block per compute unit (its stages fill LDS), a multiple of the 8 XCDs
     const int64_t cus = (device_cu_count() + 7) / 8 * 8;
     const int64_t grid = tiles < cus ? (tiles + 7) / 8 * 8 : cus;
-    hipLaunchKernelGGL((train_gemm_tiles<P, BM, NS>), dim3((uint32_t)grid), dim3(kTileThreads), 0, stream, p, n_tiles);
+    hipLaunchKernelGGL((train_gemm_tiles<P, S>), dim3((uint32_t)grid), dim3(S::kThreads), 0, stream, p, n_tiles);
     return hipGetLastError();
 }
 
@@ -531,8 +506,8 @@ template <TrainProduct P>
 hipError_t launch_product(const TrainGemmArgs &p, hipStream_t stream)
 {
     if (p.max_rows / p.E >= 512)
-        return launch_tiles<P, 256, 2>(p, stream);
-    return launch_tiles<P, 128, 3>(p, stream);
+        return launch_tiles<P, Rows256>(p, stream);
+    return launch_tiles<P, Rows128>(p, stream);
 }
 
 }  // namespace

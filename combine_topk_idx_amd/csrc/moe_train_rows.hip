@@ -97,19 +97,21 @@ __global__ __launch_bounds__(kBlockThreads) void activation_backward_kernel(ActB
             g.values(gv);
             if constexpr (GATED)
                 u.values(uv);
+            dev::for_act(a.act, [&](auto act) {
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                float f, slope;
-                dev::act_both(a.act, gv[j], f, slope);
-                if constexpr (GATED) {
-                    dg[j] = dy[j] * uv[j] * slope;
-                    du[j] = dy[j] * f;
-                    y[j] = f * uv[j];
-                } else {
-                    dg[j] = dy[j] * slope;
-                    y[j] = f;
+                for (int j = 0; j < 8; ++j) {
+                    float f, slope;
+                    dev::act_both<decltype(act)::value>(gv[j], f, slope);
+                    if constexpr (GATED) {
+                        dg[j] = dy[j] * uv[j] * slope;
+                        du[j] = dy[j] * f;
+                        y[j] = f * uv[j];
+                    } else {
+                        dg[j] = dy[j] * slope;
+                        y[j] = f;
+                    }
                 }
-            }
+            });
             *reinterpret_cast<uint4 *>(a.dsaved + row * m + c) = pack8(dg);
             if constexpr (GATED)
                 *reinterpret_cast<uint4 *>(a.dsaved + row * m + a.n + c) = pack8(du);

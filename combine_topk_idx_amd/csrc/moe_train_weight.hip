@@ -2,7 +2,7 @@
 //
 //   dw[e, j, c] = sum over rows of e of dy[row, j] a[row, c],  dbias[e, j] = sum of dy[row, j]
 //
-// A block holds 256 x 256 of one expert's weights and walks its rows, 64 a step.
+// A block holds 256 x 256 of one expert's weights and walks its rows, 32 a step.
 // Both operands are summed over their slow axis: the stages hold them as they lie
 // in memory and ds_read_b64_tr_b16 hands each lane four rows of one channel.
 // dbias comes from the same fragments, times ones.
@@ -16,10 +16,9 @@ namespace {
 using namespace tile;
 using namespace tile::train;
 
-constexpr int kTileM = 256;  // channels of dy per block
-constexpr int kStageBytes = (kTileM + kTileN) * kStep * 2;
-constexpr int kHalf = kTileM * kStep * 2;  // a's channels follow dy's
-constexpr int MT = kTileM / 16 / kWaveRows;
+using S = TileShape<256, 2, 2, 32, 4>;  // its rows are channels of dy
+constexpr int kTileM = S::BM;  // channels of dy per block
+constexpr int MT = S::MT, NF = S::NF, kStep = S::kStep, kHalf = S::kW;
 
 struct WeightTile {
     int32_t e, split, mt, nt, rows;
@@ -62,11 +61,12 @@ struct Rows8<MOE_QUANT_NONE> {};
 // are read as zeros, and so are channels past the last.
 template <int QUANT>
 struct WeightLoads {
+    static constexpr int kRowsPerPass = 2 * S::kWaves;
     const uint16_t *dy;
     const uint8_t *a, *scale;
     uint32_t so, sstep, to;  // 8 bits: this lane's first scale, and its place in a stage
-    uint32_t yo, ao;     // this lane's place in its first row
-    uint32_t ystep, astep;  // 16 rows further
+    uint32_t yo[2], ao[2];  // this lane's place in its first rows
+    uint32_t ystep, astep;  // two passes of all waves further (8 bits: one)
     int32_t rows, n, k, wave;
 
     __device__ __forceinline__ void set(const GradWeightArgs &p, const WeightTile &at, int wave_, int lane)
@@ -77,26 +77,26 @@ struct WeightLoads {
         k = p.k;
         dy = p.dy + at.row0 * n;
         a = static_cast<const uint8_t *>(p.a) + at.row0 * k * (QUANT == MOE_QUANT_NONE ? 2 : 1);
-        // 32 bytes (16 channels) of row s sit at position c ^ (s & 3 | s >> 1 & 4) of
-        // its 512: what 32 lanes read at once then covers all banks.  A wave loads
-        // rows 2 j and 2 j + 1, j = wave (mod 8).
-        const int s = 2 * wave + (lane >> 5);
-        const int f = (s & 3) | ((s >> 1) & 4);
-        const int32_t c = ((((lane & 31) >> 1) ^ f) * 2 + (lane & 1)) * 8;
-        const int32_t j = at.mt * kTileM + c, i = at.nt * kTileN + c;
-        yo = j < n ? (uint32_t)s * (uint32_t)n * 2 + (uint32_t)j * 2 : 0x80000000u;
-        ao = i < k ? (uint32_t)s * (uint32_t)k * 2 + (uint32_t)i * 2 : 0x80000000u;
-        ystep = 32u * (uint32_t)n;
-        astep = 32u * (uint32_t)k;
+#pragma unroll
+        for (int odd = 0; odd < 2; ++odd) {  // passes by turns
+            const int s = StepPlaces::step(wave + odd * S::kWaves, lane);
+            const int32_t c = StepPlaces::channel(wave + odd * S::kWaves, lane);
+            const int32_t j = at.mt * kTileM + c, i = at.nt * kTileN + c;
+            yo[odd] = j < n ? (uint32_t)s * (uint32_t)n * 2 + (uint32_t)j * 2 : 0x80000000u;
+            ao[odd] = i < k ? (uint32_t)s * (uint32_t)k * 2 + (uint32_t)i * 2 : 0x80000000u;
+        }
+        ystep = 4u * kRowsPerPass * (uint32_t)n;
+        astep = 4u * kRowsPerPass * (uint32_t)k;
         if constexpr (QUANT != MOE_QUANT_NONE) {
+            const int s = StepPlaces::step(wave, lane);
             const int32_t piece = lane & 31, at_c = at.nt * kTileN + piece * 8;
-            ao = at_c < k ? (uint32_t)s * (uint32_t)k + (uint32_t)at_c : 0x80000000u;
-            astep = 16u * (uint32_t)k;
+            ao[0] = at_c < k ? (uint32_t)s * (uint32_t)k + (uint32_t)at_c : 0x80000000u;
+            astep = kRowsPerPass * (uint32_t)k;
             so = at_c < k ? (uint32_t)s * scale_bytes() + (uint32_t)(at_c / (QUANT == MOE_QUANT_MXFP8 ? 32 : 128)) *
                                                               (QUANT == MOE_QUANT_FP8_F32 ? 4 : 1)
                           : 0x80000000u;
-            sstep = 16u * scale_bytes();
-            to = (uint32_t)s * 512 + (((piece >> 1) ^ f) * 2 + (piece & 1)) * 16;
+            sstep = kRowsPerPass * scale_bytes();
+            to = (uint32_t)s * 512 + (((piece >> 1) ^ StepPlaces::swizzle(s)) * 2 + (piece & 1)) * 16;
             scale = static_cast<const uint8_t *>(p.a_scale) + at.row0 * scale_bytes();
         }
     }
@@ -106,198 +106,265 @@ struct WeightLoads {
         const uint32_t b = (uint32_t)k / kQuantGroup;
         return QUANT == MOE_QUANT_FP8_UE8M0 ? (b + 3) / 4 * 4 : b * 4;
     }
-    // a in 8 bits: the rows of step kb into registers, and from there into a stage.
-    __device__ __forceinline__ void fetch(Rows8<QUANT> &rows8, int kb) const
+    // a in 8 bits: pass i of step kb's rows into registers, and from there into a stage.
+    __device__ __forceinline__ void fetch(Rows8<QUANT> &rows8, int i, int kb) const
     {
         const int32_t r0 = kb * kStep;
         const uint32_t left = (uint32_t)max(0, min(kStep, rows - r0));
         const __amdgpu_buffer_rsrc_t av = buffer(a + (int64_t)r0 * k, left * (uint32_t)k);
         const __amdgpu_buffer_rsrc_t sv = buffer(scale + (int64_t)r0 * scale_bytes(), left * scale_bytes());
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            rows8.v[i] = __builtin_amdgcn_raw_buffer_load_b64(av, ao + i * astep, 0, 0);
-            if constexpr (QUANT == MOE_QUANT_FP8_F32)
-                rows8.s[i] = __builtin_amdgcn_raw_buffer_load_b32(sv, so + i * sstep, 0, 0);
-            else
-                rows8.s[i] = __builtin_amdgcn_raw_buffer_load_b8(sv, so + i * sstep, 0, 0);
-        }
+        rows8.v[i] = __builtin_amdgcn_raw_buffer_load_b64(av, ao[0] + i * astep, 0, 0);
+        if constexpr (QUANT == MOE_QUANT_FP8_F32)
+            rows8.s[i] = __builtin_amdgcn_raw_buffer_load_b32(sv, so + i * sstep, 0, 0);
+        else
+            rows8.s[i] = __builtin_amdgcn_raw_buffer_load_b8(sv, so + i * sstep, 0, 0);
     }
-    __device__ __forceinline__ void put(const Rows8<QUANT> &rows8, uint8_t *st) const
+    __device__ __forceinline__ void put(const Rows8<QUANT> &rows8, int i, uint8_t *st) const
     {
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-            *reinterpret_cast<dev::u32x4 *>(st + kHalf + to + i * 16 * 512) = rows8.bf16(i);
+        // 8 rows further the swizzle's third bit turns
+        static_assert(kRowsPerPass == 8, "rows of a pass");
+        *reinterpret_cast<dev::u32x4 *>(st + kHalf + (to ^ (i & 1) * 128) + i * kRowsPerPass * 512) = rows8.bf16(i);
     }
-    // Loads FROM .. TO - 1 of the 8 of step kb.
+    // Loads FROM .. TO - 1 of the 8 of step kb (8 bits: dy's 4).
     template <int FROM, int TO>
     __device__ __forceinline__ void issue(uint8_t *st, int kb) const
     {
         const int32_t r0 = kb * kStep;
         const uint32_t left = (uint32_t)max(0, min(kStep, rows - r0));
-#pragma unroll
-        for (int j = FROM; j < TO; ++j) {
-            const int i = j & 3;
-            if (j < 4)
-                load_lds<16>(buffer(dy + (int64_t)r0 * n, left * (uint32_t)n * 2), st + (wave + 8 * i) * 1024,
-                             yo + i * ystep, 0);
+        for_each<TO - FROM>([&](auto N) {
+            constexpr int j = FROM + decltype(N)::value, i = j % S::kA;
+            if constexpr (j < S::kA)
+                load_lds<16>(buffer(dy + (int64_t)r0 * n, left * (uint32_t)n * 2), st + (wave + S::kWaves * i) * 1024,
+                             yo[i & 1] + (i >> 1) * ystep, 0);
             else if constexpr (QUANT == MOE_QUANT_NONE)
                 load_lds<16>(buffer(a + (int64_t)r0 * k * 2, left * (uint32_t)k * 2),
-                             st + kHalf + (wave + 8 * i) * 1024, ao + i * astep, 0);
-        }
+                             st + kHalf + (wave + S::kWaves * i) * 1024, ao[i & 1] + (i >> 1) * astep, 0);
+        });
     }
 };
 
-struct WeightSums {
-    dev::f32x4 w[kNF][MT];
-    dev::f32x4 bias[MT / kWaveCols];  // the waves of a row share its fragments
+struct WeightReads {
+    int column, m0, n0;
+    __device__ __forceinline__ WeightReads(int wave, int lane)
+    {
+        column = StepPlaces::read(lane);
+        m0 = wave / S::WC * MT;
+        n0 = wave % S::WC * NF;
+    }
+    __device__ __forceinline__ dev::bf16x8 x(const uint8_t *st, int i, int) const
+    {
+        return read_steps(st + (column ^ (m0 + i) * 32));
+    }
+    __device__ __forceinline__ dev::bf16x8 w(const uint8_t *st, int f, int) const
+    {
+        return read_steps(st + kHalf + (column ^ (n0 + f) * 32));
+    }
 };
 
-template <int QUANT>
-__device__ __forceinline__ void multiply_rows(WeightSums &acc, const uint8_t *st, int wr, int wc, int lane, bool bias,
-                                              const WeightLoads<QUANT> &loads, uint8_t *free, int kb_load)
-{
-    const int r = lane & 15, g = lane >> 4;
-    const int column = (8 * g + (r >> 2)) * 2 * kTileN + ((r >> 2) | (g & 1) << 2) * 32 + (r & 3) * 8;
-    const uint8_t *rows = st, *ws = st + kHalf;
-    Fragment w[kNF], x[2];
-    x[0] = read_columns<kTileM>(rows + (column ^ (wr * MT) * 32));
-#pragma unroll
-    for (int f = 0; f < kNF; ++f)
-        w[f] = read_columns<kTileN>(ws + (column ^ (wc * 4 + f) * 32));
-    const auto part = [&](auto I) {
-        constexpr int i = decltype(I)::value;
-        if constexpr (i + 1 < MT)
-            x[(i + 1) & 1] = read_columns<kTileM>(rows + (column ^ (wr * MT + i + 1) * 32));
-#pragma unroll
-        for (int h = 0; h < 2; ++h)
-#pragma unroll
-            for (int f = 0; f < kNF; ++f)
-                acc.w[f][i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w[f].h[h], x[i & 1].h[h], acc.w[f][i], 0, 0, 0);
-        if (bias && wc == (i & (kWaveCols - 1))) {
-            const __bf16 one = (__bf16)1.0f;
-            const dev::bf16x8 ones = {one, one, one, one, one, one, one, one};
-#pragma unroll
-            for (int h = 0; h < 2; ++h)
-                acc.bias[i / kWaveCols] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(ones, x[i & 1].h[h],
-                                                                                  acc.bias[i / kWaveCols], 0, 0, 0);
-        }
-        loads.template issue<i, i + 1>(free, kb_load);
-        __builtin_amdgcn_sched_barrier(0);
-    };
-    static_assert(MT == 8, "a load per fragment of rows");
-    for_each<MT>(part);
-}
+// The waves that share a row of fragments share its sums for the bias.
+constexpr int kBias = MT / S::WC;
 
-// Results: channels 16 (MT wr + i) + (lane % 16) of dy, 4 (lane / 16) + j of
-// fragment f.  Parts of a split go to the workspace.
-__device__ __forceinline__ void write_weights(const GradWeightArgs &p, const WeightSums &acc, const WeightTile &at, int wr,
-                                              int wc, int lane)
+// Results: channels 16 (MT wr + i) .. of dy, 16 (NF wc + f) .. of a.  Parts of a
+// split go to the workspace.
+__device__ __forceinline__ void write_weights(const GradWeightArgs &p, const dev::f32x4 (&acc)[NF][MT],
+                                              const dev::f32x4 (&sums)[kBias], const WeightTile &at, int wr, int wc,
+                                              int lane)
 {
-    const int r = lane & 15, g = lane >> 4;
-    const int32_t j0 = at.mt * kTileM, c0 = at.nt * kTileN + wc * 64;
+    const int32_t j0 = at.mt * kTileM, c0 = at.nt * kTileN + wc * NF * 16;
     const int32_t valid = min(kTileM, p.n - j0);
     const bool parts = p.splits > 1;
     const int64_t group = parts ? (int64_t)at.e * p.splits + at.split : at.e;
     const int64_t first = (group * p.n + j0) * p.k;
+    const int r = lane & 15, g = lane >> 4;
     if (!parts && p.dw_bf16) {
-        const __amdgpu_buffer_rsrc_t out =
-            buffer(static_cast<uint16_t *>(p.dw) + first, (uint32_t)valid * (uint32_t)p.k * 2);
-#pragma unroll
-        for (int i = 0; i < MT; ++i) {
-            const dev::f32x4 v[kNF] = {acc.w[0][i], acc.w[1][i], acc.w[2][i], acc.w[3][i]};
-            store_lines(out, v, (wr * MT + i) * 16, valid, c0, p.k, lane);
-        }
+        const Lines out = {buffer(static_cast<uint16_t *>(p.dw) + first, (uint32_t)valid * (uint32_t)p.k * 2), valid, p.k, 0,
+                           p.k};
+        for_each<MT>([&](auto I) {
+            constexpr int i = decltype(I)::value;
+            for_each<NF / 4>([&](auto F) {
+                constexpr int f = 4 * decltype(F)::value;
+                store_lines(out, acc[f][i], acc[f + 1][i], acc[f + 2][i], acc[f + 3][i], (wr * MT + i) * 16, c0 + f * 16,
+                            lane);
+            });
+            __builtin_amdgcn_sched_barrier(0);
+        });
     } else {
-        const bool add = !parts && p.accumulate;
         const __amdgpu_buffer_rsrc_t out =
             buffer((parts ? p.partial : static_cast<float *>(p.dw)) + first, (uint32_t)valid * (uint32_t)p.k * 4);
-#pragma unroll
-        for (int i = 0; i < MT; ++i)
-#pragma unroll
-            for (int f = 0; f < kNF; ++f) {
-                const int row = (wr * MT + i) * 16 + r;
-                const int32_t c = c0 + f * 16 + 4 * g;
-                const uint32_t off = row < valid && c < p.k ? ((uint32_t)row * (uint32_t)p.k + c) * 4 : 0x80000000u;
-                dev::f32x4 v = acc.w[f][i];
-                if (add)
-                    v += __builtin_bit_cast(dev::f32x4, __builtin_amdgcn_raw_buffer_load_b128(out, off, 0, 0));
-                __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(dev::u32x4, v), out, off, 0, kStreamed);
-            }
+        const auto store = [&](auto add) {
+            for_each<MT>([&](auto I) {
+                constexpr int i = decltype(I)::value;
+                for_each<NF / 2>([&](auto F) {
+                    constexpr int f = 2 * decltype(F)::value;
+                    store_wide<decltype(add)::value>(out, acc[f][i], acc[f + 1][i], (wr * MT + i) * 16, valid, c0 + f * 16, p.k,
+                                                     lane);
+                });
+                __builtin_amdgcn_sched_barrier(0);
+            });
+        };
+        if (!parts && p.accumulate)
+            store(std::true_type());
+        else
+            store(std::false_type());
     }
     if (p.dbias != nullptr && at.nt == 0 && g == 0) {
         float *out = parts ? p.partial + (int64_t)p.E * p.splits * p.n * p.k : p.dbias;
 #pragma unroll
-        for (int b = 0; b < MT / kWaveCols; ++b) {
-            const int row = (wr * MT + b * kWaveCols + wc) * 16 + r;
+        for (int b = 0; b < kBias; ++b) {
+            const int row = (wr * MT + b * S::WC + wc) * 16 + r;
             if (row < valid) {
                 float *to = out + group * p.n + j0 + row;
-                *to = !parts && p.accumulate ? *to + acc.bias[b][0] : acc.bias[b][0];
+                *to = !parts && p.accumulate ? *to + sums[b][0] : sums[b][0];
             }
         }
     }
 }
 
+// The loads that a tile begins with: four stages, and of a in 8 bits the first two
+// through registers.
 template <int QUANT>
-__global__ __launch_bounds__(kTileThreads) void grad_weight_tiles(GradWeightArgs p, int32_t m_tiles, int32_t n_tiles)
+__device__ __forceinline__ void start_weights(const GradWeightArgs &p, const WeightTile &at, const Stages &st,
+                                              Rows8<QUANT> (&rows8)[2], int wave, int lane)
 {
-    __shared__ alignas(1024) uint8_t st0[kStageBytes];
-    __shared__ alignas(1024) uint8_t st1[kStageBytes];
+    WeightLoads<QUANT> loads;
+    loads.set(p, at, wave, lane);
+    if constexpr (QUANT != MOE_QUANT_NONE) {
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                loads.fetch(rows8[u], i, u);
+        __builtin_amdgcn_sched_barrier(0);
+    }
+    loads.template issue<0, S::kLoads>(st.s0, 0);
+    __builtin_amdgcn_sched_barrier(0);  // in this order: the waits count
+    loads.template issue<0, S::kLoads>(st.s1, 1);
+    __builtin_amdgcn_sched_barrier(0);
+    loads.template issue<0, S::kLoads>(st.s2, 2);
+    __builtin_amdgcn_sched_barrier(0);
+    loads.template issue<0, S::kLoads>(st.s3, 3);
+    __builtin_amdgcn_sched_barrier(0);
+}
+
+// Multiplies a tile whose first loads are in flight, then starts the next tile's
+// (`more`) and writes the results.
+//
+// a in 8 bits goes through registers, two steps behind its loads: rows fetched in
+// step u are put into their stage in step u + 2 and read in step u + 3.  Loads come
+// back in order, so waiting for them sooner would wait for dy's too.
+template <int QUANT, bool BIAS>
+__device__ __forceinline__ void run_weights(const GradWeightArgs &p, const WeightTile &at, const WeightTile &next, bool more,
+                                            const Stages &st, Rows8<QUANT> (&rows8)[2], int wave, int lane)
+{
+    constexpr bool k8 = QUANT != MOE_QUANT_NONE;
+    // a stage's loads that wait for LDS, and the loads of a step
+    constexpr int kDma = k8 ? S::kA : S::kLoads, kStepLoads = k8 ? kDma + 8 : kDma;
+    WeightLoads<QUANT> loads;
+    loads.set(p, at, wave, lane);
+    const WeightReads reads(wave, lane);
+    const int wr = wave / S::WC, wc = wave % S::WC;
+    const int KB = scalar((at.rows + kStep - 1) / kStep);
+    dev::f32x4 acc[NF][MT], sums[kBias];
+    clear(acc);
+#pragma unroll
+    for (int b = 0; b < kBias; ++b)
+        sums[b] = dev::f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    if constexpr (k8) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            loads.put(rows8[0], i, st.s0);
+            loads.put(rows8[1], i, st.s1);
+        }
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                loads.fetch(rows8[u], i, 2 + u);
+    }
+    Fragments<S, MT> even, odd;
+    wait_and_meet<k8 ? 3 * kDma : 3 * S::kLoads>();
+    for_each<MT + NF>([&](auto N) { read_fragment<decltype(N)::value, S, MT>(even, st.s0, 0, reads); });
+    // cur: the stage of step kb, after: kb + 1, put: kb + 2
+    const auto step = [&](Fragments<S, MT> &now, Fragments<S, MT> &then, Rows8<QUANT> &r8, uint8_t *cur, uint8_t *after,
+                          uint8_t *put, int kb) {
+        wait_and_meet<2 * kStepLoads>();
+        multiply<true, S, MT>(acc, now, then, after, 0, reads, loads, cur, kb + 4, [&](auto I, const dev::bf16x8 &x) {
+            constexpr int i = decltype(I)::value;
+            if constexpr (BIAS) {  // the waves of a row of fragments share them
+                if (wc == i % S::WC) {
+                    const __bf16 one = (__bf16)1.0f;
+                    const dev::bf16x8 ones = {one, one, one, one, one, one, one, one};
+                    mfma_beside(sums[i / S::WC], ones, x);
+                }
+            }
+            if constexpr (k8 && i < 4)
+                loads.put(r8, i, put);
+            if constexpr (k8 && i >= 4)
+                loads.fetch(r8, i - 4, kb + 4);
+        });
+    };
+    static_assert(MT == 8, "four passes of a step's rows: put, then fetched");
+    for (int kb = 0; kb < KB; kb += 4) {  // whole rounds: rows past the last are zeros
+        step(even, odd, rows8[0], st.s0, st.s1, st.s2, kb);
+        step(odd, even, rows8[1], st.s1, st.s2, st.s3, kb + 1);
+        step(even, odd, rows8[0], st.s2, st.s3, st.s0, kb + 2);
+        step(odd, even, rows8[1], st.s3, st.s0, st.s1, kb + 3);
+        end_turn(kb + 4, KB);
+    }
+    wait_and_meet<0>();
+    if (more)
+        start_weights<QUANT>(p, next, st, rows8, wave, lane);
+    write_weights(p, acc, sums, at, wr, wc, lane);
+}
+
+template <int QUANT>
+__global__ __launch_bounds__(S::kThreads, 1) void grad_weight_tiles(GradWeightArgs p, int32_t m_tiles, int32_t n_tiles)
+{
+    __shared__ alignas(1024) uint8_t st0[S::kBytes], st1[S::kBytes], st2[S::kBytes], st3[S::kBytes];
+    const Stages st = {st0, st1, st2, st3};
     const int lane = threadIdx.x & (kWave - 1);
     const int wave = scalar(threadIdx.x / kWave);
-    const int wr = wave / kWaveCols, wc = wave % kWaveCols;
-    const int64_t tiles = (int64_t)m_tiles * n_tiles;
-    const int64_t n_work = tiles * p.E * p.splits;
-    for (int64_t work = blockIdx.x; work < n_work; work += gridDim.x) {
+    const int32_t tiles = m_tiles * n_tiles;
+    const int64_t n_work = (int64_t)tiles * p.E * p.splits;
+    const auto locate = [&](int64_t work) {
         WeightTile at;
         const int32_t part = scalar((int32_t)(work / tiles));
-        const int32_t t = scalar((int32_t)(work - part * tiles));
+        const int32_t t = scalar((int32_t)(work - (int64_t)part * tiles));
         at.e = scalar(part / p.splits);
-        at.split = part - at.e * p.splits;
+        at.split = scalar(part - at.e * p.splits);
         at.nt = scalar(t / m_tiles);
-        at.mt = t - at.nt * m_tiles;
+        at.mt = scalar(t - at.nt * m_tiles);
         const int32_t rows = p.recv_count != nullptr ? word_of(p.recv_count, at.e) : p.dense_rows;
         const int32_t steps = (rows + kStep - 1) / kStep;
         const int32_t s0 = scalar((int32_t)((int64_t)steps * at.split / p.splits));
         const int32_t s1 = scalar((int32_t)((int64_t)steps * (at.split + 1) / p.splits));
         at.rows = scalar(min(rows, s1 * kStep) - min(rows, s0 * kStep));
-        at.row0 = (int64_t)(p.expert_offset != nullptr ? word_of(p.expert_offset, at.e) : 0) + s0 * kStep;
-        const bool bias = p.dbias != nullptr && at.nt == 0;
-
-        WeightLoads<QUANT> loads;
-        loads.set(p, at, wave, lane);
-        WeightSums acc;
-#pragma unroll
-        for (int i = 0; i < MT; ++i)
-#pragma unroll
-            for (int f = 0; f < kNF; ++f)
-                acc.w[f][i] = dev::f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-        for (int b = 0; b < MT / kWaveCols; ++b)
-            acc.bias[b] = dev::f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-        loads.template issue<0, 8>(st0, 0);
-        Rows8<QUANT> rows8;
-        if constexpr (QUANT != MOE_QUANT_NONE) {
-            loads.fetch(rows8, 0);
-            loads.put(rows8, st0);
-        }
-        const int KB = s1 - s0;
-        const auto step = [&](uint8_t *cur, uint8_t *free, int kb) {
-            wait_and_meet<0>();
-            if constexpr (QUANT != MOE_QUANT_NONE)
-                loads.fetch(rows8, kb + 1);
-            multiply_rows<QUANT>(acc, cur, wr, wc, lane, bias, loads, free, kb + 1);
-            if constexpr (QUANT != MOE_QUANT_NONE)
-                loads.put(rows8, free);
-        };
-        int kb = 0;
-        for (; kb + 2 <= KB; kb += 2) {
-            step(st0, st1, kb);
-            step(st1, st0, kb + 1);
-        }
-        if (kb < KB)
-            step(st0, st1, kb);
-        write_weights(p, acc, at, wr, wc, lane);
-        wait_and_meet<0>();  // the next tile loads into both stages
+        at.row0 = (int64_t)(p.expert_offset != nullptr ? word_of(p.expert_offset, at.e) : 0) + (int64_t)s0 * kStep;
+        return at;
+    };
+    // workgroups go to the 8 XCDs in turn: each XCD takes a contiguous run of
+    // the work, so that the tiles of one expert share its L2
+    const int64_t run = (n_work + 7) / 8;
+    const int64_t base = (int64_t)(blockIdx.x & 7) * run;
+    const int64_t end = min(run, n_work - base);
+    int64_t idx = blockIdx.x >> 3;
+    if (idx >= end)
+        return;
+    Rows8<QUANT> rows8[2];
+    WeightTile next = locate(base + idx);
+    start_weights<QUANT>(p, next, st, rows8, wave, lane);
+    for (;;) {
+        const WeightTile at = next;
+        idx += gridDim.x >> 3;
+        const bool more = idx < end;
+        if (more)
+            next = locate(base + idx);
+        if (p.dbias != nullptr && at.nt == 0)
+            run_weights<QUANT, true>(p, at, next, more, st, rows8, wave, lane);
+        else
+            run_weights<QUANT, false>(p, at, next, more, st, rows8, wave, lane);
+        if (!more)
+            break;
     }
 }
 
@@ -329,7 +396,7 @@ __global__ __launch_bounds__(kBlockThreads) void grad_weight_join(GradWeightArgs
 int32_t grad_weight_splits(int64_t max_rows, int32_t E, int32_t n, int32_t k)
 {
     const int64_t tiles = (int64_t)E * ((n + kTileM - 1) / kTileM) * ((k + kTileN - 1) / kTileN);
-    const int64_t steps = max_rows / E / kStep;  // of an expert, evenly routed
+    const int64_t steps = max_rows / E / 64;  // of an expert, evenly routed
     const int64_t splits = tiles >= 128 ? 1 : 256 / tiles;
     return (int32_t)(splits < steps / 8 ? splits : steps / 8 < 1 ? 1 : steps / 8);
 }
@@ -338,8 +405,9 @@ hipError_t launch_grad_weight(const GradWeightArgs &p, hipStream_t stream)
 {
     const int32_t m_tiles = (p.n + kTileM - 1) / kTileM, n_tiles = (p.k + kTileN - 1) / kTileN;
     const int64_t work = (int64_t)m_tiles * n_tiles * p.E * p.splits;
-    const int64_t cus = device_cu_count();
-    const dim3 grid((uint32_t)(work < cus ? work : cus)), block(kTileThreads);
+    // one block per compute unit (its stages fill LDS), a multiple of the 8 XCDs
+    const int64_t cus = (device_cu_count() + 7) / 8 * 8;
+    const dim3 grid((uint32_t)(work < cus ? (work + 7) / 8 * 8 : cus)), block(S::kThreads);
     switch (p.a_quant) {
     case MOE_QUANT_FP8_F32:
         hipLaunchKernelGGL((grad_weight_tiles<MOE_QUANT_FP8_F32>), grid, block, 0, stream, p, m_tiles, n_tiles);
