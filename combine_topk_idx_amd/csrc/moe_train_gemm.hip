@@ -54,8 +54,8 @@ struct TileLoads {
 #pragma unroll
             for (int odd = 0; odd < 2; ++odd) {  // passes by turns
                 const int n = wave + odd * S::kWaves;
-                const int32_t c = at.nt * kTileN + StepPlaces::channel(n, lane);
-                wo[odd] = c < p.k ? (uint32_t)StepPlaces::step(n, lane) * (uint32_t)stride * 2 + (uint32_t)c * 2 : 0x80000000u;
+                const int32_t c = at.nt * kTileN + StepPlaces<kTileN>::channel(n, lane);
+                wo[odd] = c < p.k ? (uint32_t)StepPlaces<kTileN>::step(n, lane) * (uint32_t)stride * 2 + (uint32_t)c * 2 : 0x80000000u;
             }
             we = p.w + (int64_t)at.e * p.n * p.k;
         } else {
@@ -109,7 +109,7 @@ struct TileReads {
         row = RowPlaces<S>::read(lane);
         rows = wave / S::WC * MT * 16 * S::kRow;
         channels = wave % S::WC;
-        column = StepPlaces::read(lane);
+        column = StepPlaces<kTileN>::read(lane);
     }
     // 16 rows, or 16 channels, of half h of a step.
     __device__ __forceinline__ dev::bf16x8 x(const uint8_t *st, int i, int h) const
@@ -119,7 +119,7 @@ struct TileReads {
     __device__ __forceinline__ dev::bf16x8 w(const uint8_t *st, int f, int h) const
     {
         if constexpr (P == kGradInput)
-            return read_steps(st + S::kW + (column ^ (channels * S::NF + f) * 32) + h * 64 * kTileN);
+            return read_steps<kTileN>(st + S::kW + (column ^ (channels * S::NF + f) * 32) + h * 64 * kTileN);
         // gated: the first half of a wave's fragments are gate channels
         constexpr int kHalf = S::NF / 2;
         const int c = P == kGated ? (channels * kHalf + f % kHalf) * 16 + f / kHalf * 128 : (channels * S::NF + f) * 16;
@@ -365,7 +365,7 @@ __device__ __forceinline__ void run_tile(const TrainGemmArgs &p, const TileAt &a
     if constexpr (S::kStages == 3) {
         const auto step = [&](uint8_t *cur, uint8_t *free, int kb) {
             wait_and_meet<S::kLoads>();
-            multiply_stage<S, MT>(acc, cur, reads, loads, free, kb + 2);
+            multiply_stage<S, MT>(acc, cur, reads, loads, free, kb + 2, [](auto) {});
         };
         // The first steps stand before the loop: there the compiler's own waits allow
         // for the stores of the tile before, in the loop they would hold up each turn.
@@ -388,11 +388,10 @@ __device__ __forceinline__ void run_tile(const TrainGemmArgs &p, const TileAt &a
         // halves the waves meet: the next stage is there and this one has been read, so
         // the step after next loads into it.
         Fragments<S, MT> first, second;
-        const auto none = [](auto, const dev::bf16x8 &) {};
         const auto step = [&](uint8_t *cur, uint8_t *other, int kb) {
-            multiply<false, S, MT>(acc, first, second, cur, 1, reads, loads, cur, 0, none);
+            multiply<false, S, MT>(acc, first, second, cur, 1, reads, loads, cur, 0);
             wait_and_meet<0>();
-            multiply<true, S, MT>(acc, second, first, other, 0, reads, loads, cur, kb + 2, none);
+            multiply<true, S, MT>(acc, second, first, other, 0, reads, loads, cur, kb + 2);
         };
         wait_and_meet<S::kLoads>();
         for_each<MT + S::NF>([&](auto N) { read_fragment<decltype(N)::value, S, MT>(first, st.s0, 0, reads); });

@@ -63,25 +63,27 @@ struct RowPlaces {
     }
 };
 
-// ---- an operand whose rows are the summed steps, 512 bytes of 256 channels -------------
+// ---- an operand whose rows are the summed steps, 256 or 128 channels of them -----------
 //
 // 32 bytes (16 channels) c of step s sit at position c ^ (s % 4 + s / 8 % 2 * 4):
-// what 32 lanes read at once then covers all banks.  A load has two steps.
+// what 32 lanes read at once then covers all banks.  A load has 1 KB, two or four steps.
 // ds_read_b64_tr_b16 hands each of 16 lanes 4 steps of one of 16 channels.
 
+template <int COLS>
 struct StepPlaces {
+    static constexpr int kLanes = COLS / 8, kSteps = kWave / kLanes;  // lanes of a step, steps of a load
     static __device__ __forceinline__ int swizzle(int s) { return (s & 3) | ((s >> 1) & 4); }
-    // This lane's step and channel in a load of steps 2 n and 2 n + 1.
-    static __device__ __forceinline__ int step(int n, int lane) { return 2 * n + (lane >> 5); }
+    // This lane's step and channel in load n.
+    static __device__ __forceinline__ int step(int n, int lane) { return kSteps * n + lane / kLanes; }
     static __device__ __forceinline__ int channel(int n, int lane)
     {
-        return ((((lane & 31) >> 1) ^ swizzle(step(n, lane))) * 2 + (lane & 1)) * 8;
+        return ((((lane & (kLanes - 1)) >> 1) ^ swizzle(step(n, lane))) * 2 + (lane & 1)) * 8;
     }
     // This lane's place in a fragment's first step; fragment f: ^ 32 f.
     static __device__ __forceinline__ int read(int lane)
     {
         const int s = 8 * (lane >> 4) + ((lane >> 2) & 3);
-        return s * 2 * kTileN + swizzle(s) * 32 + (lane & 3) * 8;
+        return s * 2 * COLS + swizzle(s) * 32 + (lane & 3) * 8;
     }
 };
 
@@ -89,12 +91,13 @@ typedef short s16x4 __attribute__((ext_vector_type(4)));
 typedef short s16x8 __attribute__((ext_vector_type(8)));
 
 // 16 channels of 32 steps from `at`, this lane's place in the first.
+template <int COLS>
 __device__ __forceinline__ dev::bf16x8 read_steps(const uint8_t *at)
 {
     const auto four = [](const uint8_t *p) {
         return __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4 *)p);
     };
-    const s16x4 lo = four(at), hi = four(at + 8 * kTileN);
+    const s16x4 lo = four(at), hi = four(at + 8 * COLS);
     return __builtin_bit_cast(dev::bf16x8, (s16x8)__builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
 }
 
@@ -130,14 +133,6 @@ __device__ __forceinline__ void mfma_in_place(dev::f32x4 &acc, const dev::bf16x8
         : "v"(__builtin_bit_cast(dev::u32x4, w)), "v"(__builtin_bit_cast(dev::u32x4, x)));
 }
 
-// The same for a sum outside the accumulators, and w from anywhere.
-__device__ __forceinline__ void mfma_beside(dev::f32x4 &sum, const dev::bf16x8 &w, const dev::bf16x8 &x)
-{
-    asm("s_nop 1\n\tv_mfma_f32_16x16x32_bf16 %0, %1, %2, %0"
-        : "+v"(sum)
-        : "v"(__builtin_bit_cast(dev::u32x4, w)), "v"(__builtin_bit_cast(dev::u32x4, x)));
-}
-
 // The end of a loop of them: when it is the last turn (at >= end, uniform), the wait
 // before a sum is read or moved (at most 19 cycles).  It has to stand here, in one
 // piece with the loop: the compiler may move sums as soon as the loop is left.
@@ -153,12 +148,11 @@ __device__ __forceinline__ void end_turn(int at, int end)
 // into `next` and, with LOAD, step `kb_load` loads into the stage `free`.  One wave
 // has the SIMD: what is issued between two matrix instructions has to fit beside
 // one, so reads and loads stand one by one among them, the reads first (loads all
-// at once in the first half: 12% slower).  extra(i, x): more to do after row
-// fragment i.
-template <bool LOAD, typename S, int MT, typename Reads, typename Loads, typename Extra>
+// at once in the first half: 12% slower).
+template <bool LOAD, typename S, int MT, typename Reads, typename Loads>
 __device__ __forceinline__ void multiply(dev::f32x4 (&acc)[S::NF][MT], const Fragments<S, MT> &now, Fragments<S, MT> &next,
                                          const uint8_t *st, int h, const Reads &reads, const Loads &loads, uint8_t *free,
-                                         int kb_load, const Extra &extra)
+                                         int kb_load)
 {
     constexpr int kAll = MT * S::NF, kReads = MT + S::NF, kGap = kAll / kReads > 3 ? 3 : kAll / kReads;
     for_each<kAll>([&](auto Q) {
@@ -168,37 +162,34 @@ __device__ __forceinline__ void multiply(dev::f32x4 (&acc)[S::NF][MT], const Fra
         if constexpr (LOAD)
             loads.template issue<q * S::kLoads / kAll, (q + 1) * S::kLoads / kAll>(free, kb_load);
         mfma_in_place(acc[f][i], now.w[f], now.x[i]);
-        if constexpr (f == S::NF - 1)
-            extra(std::integral_constant<int, i>(), now.x[i]);
         __builtin_amdgcn_sched_barrier(0);
     });
 }
 
-// acc += the stage `st`, two waves per SIMD: fragments are read as they are needed.
-template <typename S, int MT, typename Reads, typename Loads>
+// acc += the stage `st`, two waves per SIMD: fragments are read as they are needed,
+// while step `kb_load` loads into the stage `free`.  extra(i): more to do after row
+// fragment i.
+template <typename S, int MT, typename Reads, typename Loads, typename Extra>
 __device__ __forceinline__ void multiply_stage(dev::f32x4 (&acc)[S::NF][MT], const uint8_t *st, const Reads &reads,
-                                               const Loads &loads, uint8_t *free, int kb_load)
+                                               const Loads &loads, uint8_t *free, int kb_load, const Extra &extra)
 {
-    dev::bf16x8 w[S::NF][2], x[2][2];
+    constexpr int H = S::kHalves;
+    dev::bf16x8 w[S::NF][H], x[2][H];
     for_each<S::NF>([&](auto F) {
         constexpr int f = decltype(F)::value;
-        w[f][0] = reads.w(st, f, 0);
-        w[f][1] = reads.w(st, f, 1);
-        if constexpr (f == 0) {
-            x[0][0] = reads.x(st, 0, 0);
-            x[0][1] = reads.x(st, 0, 1);
-        }
+        for_each<H>([&](auto N) { w[f][decltype(N)::value] = reads.w(st, f, decltype(N)::value); });
+        if constexpr (f == 0)
+            for_each<H>([&](auto N) { x[0][decltype(N)::value] = reads.x(st, 0, decltype(N)::value); });
     });
     for_each<MT>([&](auto I) {
         constexpr int i = decltype(I)::value;
-        if constexpr (i + 1 < MT) {
-            x[(i + 1) & 1][0] = reads.x(st, i + 1, 0);
-            x[(i + 1) & 1][1] = reads.x(st, i + 1, 1);
-        }
-        for_each<2 * S::NF>([&](auto Q) {
+        if constexpr (i + 1 < MT)
+            for_each<H>([&](auto N) { x[(i + 1) & 1][decltype(N)::value] = reads.x(st, i + 1, decltype(N)::value); });
+        for_each<H * S::NF>([&](auto Q) {
             constexpr int h = decltype(Q)::value / S::NF, f = decltype(Q)::value % S::NF;
             acc[f][i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w[f][h], x[i & 1][h], acc[f][i], 0, 0, 0);
         });
+        extra(I);
         loads.template issue<i * S::kLoads / MT, (i + 1) * S::kLoads / MT>(free, kb_load);
         __builtin_amdgcn_sched_barrier(0);
     });

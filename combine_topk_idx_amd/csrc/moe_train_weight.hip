@@ -2,7 +2,7 @@
 //
 //   dw[e, j, c] = sum over rows of e of dy[row, j] a[row, c],  dbias[e, j] = sum of dy[row, j]
 //
-// A block holds 256 x 256 of one expert's weights and walks its rows, 32 a step.
+// A block holds 128 x 256 of one expert's weights and walks its rows, 32 a step.
 // Both operands are summed over their slow axis: the stages hold them as they lie
 // in memory and ds_read_b64_tr_b16 hands each lane four rows of one channel.
 // dbias comes from the same fragments, times ones.
@@ -16,9 +16,11 @@ namespace {
 using namespace tile;
 using namespace tile::train;
 
-using S = TileShape<256, 2, 2, 32, 4>;  // its rows are channels of dy
+using S = TileShape<128, 2, 2, 32, 3>;  // its rows are channels of dy
 constexpr int kTileM = S::BM;  // channels of dy per block
 constexpr int MT = S::MT, NF = S::NF, kStep = S::kStep, kHalf = S::kW;
+
+constexpr int kGroupM = 16;
 
 struct WeightTile {
     int32_t e, split, mt, nt, rows;
@@ -61,12 +63,14 @@ struct Rows8<MOE_QUANT_NONE> {};
 // are read as zeros, and so are channels past the last.
 template <int QUANT>
 struct WeightLoads {
-    static constexpr int kRowsPerPass = 2 * S::kWaves;
+    using Dy = StepPlaces<kTileM>;
+    using A = StepPlaces<kTileN>;
+    static constexpr int kRowsPerPass = A::kSteps * S::kWaves;
     const uint16_t *dy;
     const uint8_t *a, *scale;
     uint32_t so, sstep, to;  // 8 bits: this lane's first scale, and its place in a stage
-    uint32_t yo[2], ao[2];  // this lane's place in its first rows
-    uint32_t ystep, astep;  // two passes of all waves further (8 bits: one)
+    uint32_t yo, ao[2];     // this lane's place in its first rows
+    uint32_t ystep, astep;  // a pass of all waves further, two of a's (8 bits: one)
     int32_t rows, n, k, wave;
 
     __device__ __forceinline__ void set(const GradWeightArgs &p, const WeightTile &at, int wave_, int lane)
@@ -77,18 +81,17 @@ struct WeightLoads {
         k = p.k;
         dy = p.dy + at.row0 * n;
         a = static_cast<const uint8_t *>(p.a) + at.row0 * k * (QUANT == MOE_QUANT_NONE ? 2 : 1);
+        const int32_t j = at.mt * kTileM + Dy::channel(wave, lane);
+        yo = j < n ? (uint32_t)Dy::step(wave, lane) * (uint32_t)n * 2 + (uint32_t)j * 2 : 0x80000000u;
+        ystep = 2u * Dy::kSteps * S::kWaves * (uint32_t)n;
 #pragma unroll
         for (int odd = 0; odd < 2; ++odd) {  // passes by turns
-            const int s = StepPlaces::step(wave + odd * S::kWaves, lane);
-            const int32_t c = StepPlaces::channel(wave + odd * S::kWaves, lane);
-            const int32_t j = at.mt * kTileM + c, i = at.nt * kTileN + c;
-            yo[odd] = j < n ? (uint32_t)s * (uint32_t)n * 2 + (uint32_t)j * 2 : 0x80000000u;
-            ao[odd] = i < k ? (uint32_t)s * (uint32_t)k * 2 + (uint32_t)i * 2 : 0x80000000u;
+            const int32_t i = at.nt * kTileN + A::channel(wave + odd * S::kWaves, lane);
+            ao[odd] = i < k ? (uint32_t)A::step(wave + odd * S::kWaves, lane) * (uint32_t)k * 2 + (uint32_t)i * 2 : 0x80000000u;
         }
-        ystep = 4u * kRowsPerPass * (uint32_t)n;
         astep = 4u * kRowsPerPass * (uint32_t)k;
         if constexpr (QUANT != MOE_QUANT_NONE) {
-            const int s = StepPlaces::step(wave, lane);
+            const int s = A::step(wave, lane);
             const int32_t piece = lane & 31, at_c = at.nt * kTileN + piece * 8;
             ao[0] = at_c < k ? (uint32_t)s * (uint32_t)k + (uint32_t)at_c : 0x80000000u;
             astep = kRowsPerPass * (uint32_t)k;
@@ -96,7 +99,7 @@ struct WeightLoads {
                                                               (QUANT == MOE_QUANT_FP8_F32 ? 4 : 1)
                           : 0x80000000u;
             sstep = kRowsPerPass * scale_bytes();
-            to = (uint32_t)s * 512 + (((piece >> 1) ^ StepPlaces::swizzle(s)) * 2 + (piece & 1)) * 16;
+            to = (uint32_t)s * 512 + (((piece >> 1) ^ A::swizzle(s)) * 2 + (piece & 1)) * 16;
             scale = static_cast<const uint8_t *>(p.a_scale) + at.row0 * scale_bytes();
         }
     }
@@ -132,10 +135,10 @@ struct WeightLoads {
         const int32_t r0 = kb * kStep;
         const uint32_t left = (uint32_t)max(0, min(kStep, rows - r0));
         for_each<TO - FROM>([&](auto N) {
-            constexpr int j = FROM + decltype(N)::value, i = j % S::kA;
+            constexpr int j = FROM + decltype(N)::value, i = j < S::kA ? j : j - S::kA;
             if constexpr (j < S::kA)
                 load_lds<16>(buffer(dy + (int64_t)r0 * n, left * (uint32_t)n * 2), st + (wave + S::kWaves * i) * 1024,
-                             yo[i & 1] + (i >> 1) * ystep, 0);
+                             yo + i * ystep, 0);
             else if constexpr (QUANT == MOE_QUANT_NONE)
                 load_lds<16>(buffer(a + (int64_t)r0 * k * 2, left * (uint32_t)k * 2),
                              st + kHalf + (wave + S::kWaves * i) * 1024, ao[i & 1] + (i >> 1) * astep, 0);
@@ -144,20 +147,21 @@ struct WeightLoads {
 };
 
 struct WeightReads {
-    int column, m0, n0;
+    int row, column, m0, n0;
     __device__ __forceinline__ WeightReads(int wave, int lane)
     {
-        column = StepPlaces::read(lane);
+        row = StepPlaces<kTileM>::read(lane);
+        column = StepPlaces<kTileN>::read(lane);
         m0 = wave / S::WC * MT;
         n0 = wave % S::WC * NF;
     }
     __device__ __forceinline__ dev::bf16x8 x(const uint8_t *st, int i, int) const
     {
-        return read_steps(st + (column ^ (m0 + i) * 32));
+        return read_steps<kTileM>(st + (row ^ (m0 + i) * 32));
     }
     __device__ __forceinline__ dev::bf16x8 w(const uint8_t *st, int f, int) const
     {
-        return read_steps(st + kHalf + (column ^ (n0 + f) * 32));
+        return read_steps<kTileN>(st + kHalf + (column ^ (n0 + f) * 32));
     }
 };
 
@@ -211,7 +215,7 @@ __device__ __forceinline__ void write_weights(const GradWeightArgs &p, const dev
         float *out = parts ? p.partial + (int64_t)p.E * p.splits * p.n * p.k : p.dbias;
 #pragma unroll
         for (int b = 0; b < kBias; ++b) {
-            const int row = (wr * MT + b * S::WC + wc) * 16 + r;
+            const int row = (wr * MT + wc * kBias + b) * 16 + r;
             if (row < valid) {
                 float *to = out + group * p.n + j0 + row;
                 *to = !parts && p.accumulate ? *to + sums[b][0] : sums[b][0];
@@ -220,44 +224,36 @@ __device__ __forceinline__ void write_weights(const GradWeightArgs &p, const dev
     }
 }
 
-// The loads that a tile begins with: four stages, and of a in 8 bits the first two
-// through registers.
+// The loads that a tile begins with: two stages, a in 8 bits through registers.
 template <int QUANT>
 __device__ __forceinline__ void start_weights(const GradWeightArgs &p, const WeightTile &at, const Stages &st,
-                                              Rows8<QUANT> (&rows8)[2], int wave, int lane)
+                                              Rows8<QUANT> &rows8, int wave, int lane)
 {
     WeightLoads<QUANT> loads;
     loads.set(p, at, wave, lane);
     if constexpr (QUANT != MOE_QUANT_NONE) {
 #pragma unroll
-        for (int u = 0; u < 2; ++u)
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-                loads.fetch(rows8[u], i, u);
+        for (int i = 0; i < 4; ++i)
+            loads.fetch(rows8, i, 0);
         __builtin_amdgcn_sched_barrier(0);
     }
     loads.template issue<0, S::kLoads>(st.s0, 0);
     __builtin_amdgcn_sched_barrier(0);  // in this order: the waits count
     loads.template issue<0, S::kLoads>(st.s1, 1);
     __builtin_amdgcn_sched_barrier(0);
-    loads.template issue<0, S::kLoads>(st.s2, 2);
-    __builtin_amdgcn_sched_barrier(0);
-    loads.template issue<0, S::kLoads>(st.s3, 3);
-    __builtin_amdgcn_sched_barrier(0);
 }
 
 // Multiplies a tile whose first loads are in flight, then starts the next tile's
 // (`more`) and writes the results.
 //
-// a in 8 bits goes through registers, two steps behind its loads: rows fetched in
-// step u are put into their stage in step u + 2 and read in step u + 3.  Loads come
-// back in order, so waiting for them sooner would wait for dy's too.
+// a in 8 bits goes through registers: rows fetched in step u are put into their
+// stage in step u + 1 and read in step u + 2.
 template <int QUANT, bool BIAS>
 __device__ __forceinline__ void run_weights(const GradWeightArgs &p, const WeightTile &at, const WeightTile &next, bool more,
-                                            const Stages &st, Rows8<QUANT> (&rows8)[2], int wave, int lane)
+                                            const Stages &st, Rows8<QUANT> &rows8, int wave, int lane)
 {
     constexpr bool k8 = QUANT != MOE_QUANT_NONE;
-    // a stage's loads that wait for LDS, and the loads of a step
+    // a stage's loads that go to LDS, and the loads of a step
     constexpr int kDma = k8 ? S::kA : S::kLoads, kStepLoads = k8 ? kDma + 8 : kDma;
     WeightLoads<QUANT> loads;
     loads.set(p, at, wave, lane);
@@ -272,44 +268,36 @@ __device__ __forceinline__ void run_weights(const GradWeightArgs &p, const Weigh
     if constexpr (k8) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            loads.put(rows8[0], i, st.s0);
-            loads.put(rows8[1], i, st.s1);
+            loads.put(rows8, i, st.s0);
+            loads.fetch(rows8, i, 1);
         }
-#pragma unroll
-        for (int u = 0; u < 2; ++u)
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-                loads.fetch(rows8[u], i, 2 + u);
+        __builtin_amdgcn_sched_barrier(0);
     }
-    Fragments<S, MT> even, odd;
-    wait_and_meet<k8 ? 3 * kDma : 3 * S::kLoads>();
-    for_each<MT + NF>([&](auto N) { read_fragment<decltype(N)::value, S, MT>(even, st.s0, 0, reads); });
-    // cur: the stage of step kb, after: kb + 1, put: kb + 2
-    const auto step = [&](Fragments<S, MT> &now, Fragments<S, MT> &then, Rows8<QUANT> &r8, uint8_t *cur, uint8_t *after,
-                          uint8_t *put, int kb) {
-        wait_and_meet<2 * kStepLoads>();
-        multiply<true, S, MT>(acc, now, then, after, 0, reads, loads, cur, kb + 4, [&](auto I, const dev::bf16x8 &x) {
+    // cur: the stage of step kb, after: kb + 1, free: kb + 2
+    const auto step = [&](uint8_t *cur, uint8_t *after, uint8_t *free, int kb) {
+        wait_and_meet<kStepLoads>();
+        if constexpr (BIAS) {  // the waves of a row of fragments share its sums, read again
+            const __bf16 one = (__bf16)1.0f;
+            const dev::bf16x8 ones = {one, one, one, one, one, one, one, one};
+#pragma unroll
+            for (int b = 0; b < kBias; ++b)
+                sums[b] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(ones, reads.x(cur, wc * kBias + b, 0), sums[b], 0, 0, 0);
+        }
+        multiply_stage<S, MT>(acc, cur, reads, loads, free, kb + 2, [&](auto I) {
             constexpr int i = decltype(I)::value;
-            if constexpr (BIAS) {  // the waves of a row of fragments share them
-                if (wc == i % S::WC) {
-                    const __bf16 one = (__bf16)1.0f;
-                    const dev::bf16x8 ones = {one, one, one, one, one, one, one, one};
-                    mfma_beside(sums[i / S::WC], ones, x);
-                }
+            if constexpr (k8) {
+                loads.put(rows8, i, after);
+                loads.fetch(rows8, i, kb + 2);
             }
-            if constexpr (k8 && i < 4)
-                loads.put(r8, i, put);
-            if constexpr (k8 && i >= 4)
-                loads.fetch(r8, i - 4, kb + 4);
         });
     };
-    static_assert(MT == 8, "four passes of a step's rows: put, then fetched");
-    for (int kb = 0; kb < KB; kb += 4) {  // whole rounds: rows past the last are zeros
-        step(even, odd, rows8[0], st.s0, st.s1, st.s2, kb);
-        step(odd, even, rows8[1], st.s1, st.s2, st.s3, kb + 1);
-        step(even, odd, rows8[0], st.s2, st.s3, st.s0, kb + 2);
-        step(odd, even, rows8[1], st.s3, st.s0, st.s1, kb + 3);
-        end_turn(kb + 4, KB);
+    static_assert(MT == 4 && S::kHalves == 1, "a pass of a step's rows beside each row fragment");
+    // Whole rounds: steps past the last multiply zeros.  Ways out between the steps would
+    // have the sums change registers where they meet.
+    for (int kb = 0; kb < KB; kb += 3) {
+        step(st.s0, st.s1, st.s2, kb);
+        step(st.s1, st.s2, st.s0, kb + 1);
+        step(st.s2, st.s0, st.s1, kb + 2);
     }
     wait_and_meet<0>();
     if (more)
@@ -318,10 +306,10 @@ __device__ __forceinline__ void run_weights(const GradWeightArgs &p, const Weigh
 }
 
 template <int QUANT>
-__global__ __launch_bounds__(S::kThreads, 1) void grad_weight_tiles(GradWeightArgs p, int32_t m_tiles, int32_t n_tiles)
+__global__ __launch_bounds__(S::kThreads, 2) void grad_weight_tiles(GradWeightArgs p, int32_t m_tiles, int32_t n_tiles)
 {
-    __shared__ alignas(1024) uint8_t st0[S::kBytes], st1[S::kBytes], st2[S::kBytes], st3[S::kBytes];
-    const Stages st = {st0, st1, st2, st3};
+    __shared__ alignas(1024) uint8_t st0[S::kBytes], st1[S::kBytes], st2[S::kBytes];
+    const Stages st = {st0, st1, st2, nullptr};
     const int lane = threadIdx.x & (kWave - 1);
     const int wave = scalar(threadIdx.x / kWave);
     const int32_t tiles = m_tiles * n_tiles;
@@ -332,8 +320,11 @@ __global__ __launch_bounds__(S::kThreads, 1) void grad_weight_tiles(GradWeightAr
         const int32_t t = scalar((int32_t)(work - (int64_t)part * tiles));
         at.e = scalar(part / p.splits);
         at.split = scalar(part - at.e * p.splits);
-        at.nt = scalar(t / m_tiles);
-        at.mt = scalar(t - at.nt * m_tiles);
+        // groups of kGroupM tiles along dy's channels walk a's together
+        const int32_t grp = scalar(t / (kGroupM * n_tiles)), in_grp = scalar(t - grp * kGroupM * n_tiles);
+        const int32_t wide = min(kGroupM, m_tiles - grp * kGroupM);
+        at.nt = scalar(in_grp / wide);
+        at.mt = scalar(grp * kGroupM + in_grp - at.nt * wide);
         const int32_t rows = p.recv_count != nullptr ? word_of(p.recv_count, at.e) : p.dense_rows;
         const int32_t steps = (rows + kStep - 1) / kStep;
         const int32_t s0 = scalar((int32_t)((int64_t)steps * at.split / p.splits));
@@ -350,7 +341,7 @@ __global__ __launch_bounds__(S::kThreads, 1) void grad_weight_tiles(GradWeightAr
     int64_t idx = blockIdx.x >> 3;
     if (idx >= end)
         return;
-    Rows8<QUANT> rows8[2];
+    Rows8<QUANT> rows8;
     WeightTile next = locate(base + idx);
     start_weights<QUANT>(p, next, st, rows8, wave, lane);
     for (;;) {
@@ -395,10 +386,12 @@ __global__ __launch_bounds__(kBlockThreads) void grad_weight_join(GradWeightArgs
 
 int32_t grad_weight_splits(int64_t max_rows, int32_t E, int32_t n, int32_t k)
 {
+    // 256 blocks, one per compute unit, of at least 512 rows: more of them write and read
+    // more parts (8191 rows, 768 x 2048, 48 tiles: 256 / 384 / 512 blocks 42 / 45 / 48 us;
+    // 2048 x 2048, 128 tiles: 81 / 93 / 88)
     const int64_t tiles = (int64_t)E * ((n + kTileM - 1) / kTileM) * ((k + kTileN - 1) / kTileN);
-    const int64_t steps = max_rows / E / 64;  // of an expert, evenly routed
-    const int64_t splits = tiles >= 128 ? 1 : 256 / tiles;
-    return (int32_t)(splits < steps / 8 ? splits : steps / 8 < 1 ? 1 : steps / 8);
+    const int64_t most = max_rows / E / 512, splits = 256 / tiles;
+    return (int32_t)(splits < 1 || most < 1 ? 1 : splits < most ? splits : most);
 }
 
 hipError_t launch_grad_weight(const GradWeightArgs &p, hipStream_t stream)
@@ -406,7 +399,7 @@ hipError_t launch_grad_weight(const GradWeightArgs &p, hipStream_t stream)
     const int32_t m_tiles = (p.n + kTileM - 1) / kTileM, n_tiles = (p.k + kTileN - 1) / kTileN;
     const int64_t work = (int64_t)m_tiles * n_tiles * p.E * p.splits;
     // one block per compute unit (its stages fill LDS), a multiple of the 8 XCDs
-    const int64_t cus = (device_cu_count() + 7) / 8 * 8;
+    const int64_t cus = (2 * device_cu_count() + 7) / 8 * 8;
     const dim3 grid((uint32_t)(work < cus ? (work + 7) / 8 * 8 : cus)), block(S::kThreads);
     switch (p.a_quant) {
     case MOE_QUANT_FP8_F32:
