@@ -54,17 +54,18 @@ struct TileLoads {
 #pragma unroll
             for (int odd = 0; odd < 2; ++odd) {  // passes by turns
                 const int n = wave + odd * S::kWaves;
-                const int32_t c = at.nt * kTileN + StepPlaces<kTileN>::channel(n, lane);
-                wo[odd] = c < p.k ? (uint32_t)StepPlaces<kTileN>::step(n, lane) * (uint32_t)stride * 2 + (uint32_t)c * 2 : 0x80000000u;
+                const int32_t c = at.nt * S::BN + StepPlaces<S::BN>::channel(n, lane);
+                wo[odd] = c < p.k ? (uint32_t)StepPlaces<S::BN>::step(n, lane) * (uint32_t)stride * 2 + (uint32_t)c * 2 : 0x80000000u;
             }
             we = p.w + (int64_t)at.e * p.n * p.k;
         } else {
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-                // gated: 128 gate channels, then the up channels of the same h
+                // gated: half a tile of gate channels, then the up channels of the same h
+                constexpr int kHalf = S::BN / 2;
                 const int32_t of = P == kGated ? p.n / 2 : p.n;
-                const int32_t c = min(P == kGated ? at.nt * 128 : at.nt * kTileN + h * 128, of - 1);
-                const int32_t left = min(128, of - c);
+                const int32_t c = min(P == kGated ? at.nt * kHalf : at.nt * S::BN + h * kHalf, of - 1);
+                const int32_t left = min(kHalf, of - c);
                 w[h] = buffer(p.w + ((int64_t)at.e * p.n + (P == kGated ? h * of : 0) + c) * K,
                               (uint32_t)left * row_bytes);
 #pragma unroll
@@ -90,7 +91,7 @@ struct TileLoads {
                 if constexpr (P == kGradInput) {
                     const __amdgpu_buffer_rsrc_t ws =
                         buffer(we + (int64_t)k0 * stride, (uint32_t)max(0, min(S::kStep, K - k0)) * (uint32_t)stride * 2);
-                    load_lds<16>(ws, to, wo[i & 1] + (uint32_t)(i >> 1) * 4 * S::kWaves * (uint32_t)stride * 2, 0);
+                    load_lds<16>(ws, to, wo[i & 1] + (uint32_t)(i >> 1) * 2 * StepPlaces<S::BN>::kSteps * S::kWaves * (uint32_t)stride * 2, 0);
                 } else {
                     load_lds<16>(w[i / (S::kB / 2)], to, wo[i] | past, at_k);
                 }
@@ -109,7 +110,7 @@ struct TileReads {
         row = RowPlaces<S>::read(lane);
         rows = wave / S::WC * MT * 16 * S::kRow;
         channels = wave % S::WC;
-        column = StepPlaces<kTileN>::read(lane);
+        column = StepPlaces<S::BN>::read(lane);
     }
     // 16 rows, or 16 channels, of half h of a step.
     __device__ __forceinline__ dev::bf16x8 x(const uint8_t *st, int i, int h) const
@@ -119,10 +120,10 @@ struct TileReads {
     __device__ __forceinline__ dev::bf16x8 w(const uint8_t *st, int f, int h) const
     {
         if constexpr (P == kGradInput)
-            return read_steps<kTileN>(st + S::kW + (column ^ (channels * S::NF + f) * 32) + h * 64 * kTileN);
+            return read_steps<S::BN>(st + S::kW + (column ^ (channels * S::NF + f) * 32) + h * 64 * S::BN);
         // gated: the first half of a wave's fragments are gate channels
         constexpr int kHalf = S::NF / 2;
-        const int c = P == kGated ? (channels * kHalf + f % kHalf) * 16 + f / kHalf * 128 : (channels * S::NF + f) * 16;
+        const int c = P == kGated ? (channels * kHalf + f % kHalf) * 16 + f / kHalf * (S::BN / 2) : (channels * S::NF + f) * 16;
         return *reinterpret_cast<const dev::bf16x8 *>(st + S::kW + c * S::kRow + (row ^ h * 64));
     }
 };
@@ -178,7 +179,7 @@ __device__ __forceinline__ void save_quantized(const TrainGemmArgs &p, const dev
         }
 #pragma unroll
         for (int f = 0; f < B::kOwn; f += 2) {
-            const int32_t c = at.nt * (kTileN / B::kHalves) + (wc * B::kOwn + f) * 16;
+            const int32_t c = at.nt * (S::BN / B::kHalves) + (wc * B::kOwn + f) * 16;
             const bool inside = row < at.valid && c < half;
             const int32_t channel = c + h * half;
             const dev::f32x4 *of = &v[h * B::kOwn + f];
@@ -236,7 +237,7 @@ __device__ __forceinline__ void write_tile(const TrainGemmArgs &p, const dev::f3
     const int g = lane >> 4;
     const int32_t channels = P == kGated ? p.n / 2 : P == kGradInput ? p.k : p.n;
     // this wave's channels (gated: of a half)
-    const int32_t c0 = P == kGated ? at.nt * 128 + wc * (NF / 2) * 16 : at.nt * kTileN + wc * NF * 16;
+    const int32_t c0 = P == kGated ? at.nt * (S::BN / 2) + wc * (NF / 2) * 16 : at.nt * S::BN + wc * NF * 16;
     const uint32_t bytes = (uint32_t)at.valid * (uint32_t)channels * 2;
     const Lines out = {buffer(p.y + at.row0 * channels, bytes), at.valid, channels, 0, channels};
     Lines saved, residual;
@@ -332,11 +333,11 @@ __device__ __forceinline__ void write_tile(const TrainGemmArgs &p, const dev::f3
 }
 
 // 128 rows: eight waves, two per SIMD, three stages of which two are in flight.
-using Rows128 = TileShape<128, 2, 4, 64, 3>;
+using Rows128 = TileShape<128, 256, 2, 4, 64, 3>;
 // 256 rows: four waves, one per SIMD, each with 128 x 128: the LDS reads of a
 // matrix instruction fall to two thirds of what eight waves of 128 x 64 need, which
 // together with the loads' writes would keep LDS as busy as the matrix cores.
-using Rows256 = TileShape<256, 2, 2, 64, 2>;
+using Rows256 = TileShape<256, 256, 2, 2, 64, 2>;
 
 // Starts the loads of a tile's first two stages.
 template <TrainProduct P, typename S>
@@ -479,6 +480,161 @@ __global__ __launch_bounds__(S::kThreads, 1) void train_gemm_tiles(TrainGemmArgs
     }
 }
 
+// ---------------------------------------------------------------------------
+// Few rows and too few tiles for the chip: 16 R rows x 16 weight rows (16 channels,
+// or 8 gate and 8 up channels) per block, whose waves share the summed channels, 64
+// at a time, and add up in LDS, in order.
+//
+// Bound by latency and the weights' bytes: the tiles above would leave most compute
+// units idle, with one step's round trip to memory after the other.
+// ---------------------------------------------------------------------------
+
+constexpr int kStripWaves = 8;
+
+template <TrainProduct P, int R>
+__global__ __launch_bounds__(kStripWaves *kWave) void train_gemm_strips(TrainGemmArgs p, int32_t strips)
+{
+    __shared__ int32_t tile_start[kMaxExperts / kGroup + 1];
+    __shared__ int32_t red[kStripWaves];
+    __shared__ dev::f32x4 part[kStripWaves][R][kWave];
+    constexpr int kStripRows = 16 * R, kChannels = P == kGated ? 8 : 16;
+    const int lane = threadIdx.x & (kWave - 1);
+    const int wave = scalar(threadIdx.x / kWave);
+    const int r = lane & 15, g = lane >> 4;
+    const int32_t K = p.k, half = p.n / 2;
+    const int32_t channels = P == kGated ? half : p.n;
+    const int KB = (K + 63) / 64, whole = K / 64;
+    scan_tiles<kStripRows, kStripWaves * kWave>(p, tile_start, red);
+    const int64_t n_work = (int64_t)scalar(tile_start[(p.E + kGroup - 1) / kGroup]) * strips;
+
+    for (int64_t work = blockIdx.x; work < n_work; work += gridDim.x) {
+        const int32_t m = scalar((int32_t)(work / strips));
+        const int32_t c0 = scalar((int32_t)(work - (int64_t)m * strips)) * kChannels;
+        const ExpertAt ex = find_expert<kStripRows>(p, tile_start, m);
+        const int32_t first = (m - ex.start) * kStripRows, valid = min(kStripRows, ex.rows - first);
+        const int64_t row0 = (int64_t)(p.expert_offset != nullptr ? word_of(p.expert_offset, ex.e) : 0) + first;
+        // rows past the end: the last one, channels past the end: the last one
+        const int32_t c = P == kGated ? c0 + (r & 7) + (r >> 3) * half : min(c0 + r, p.n - 1);
+        const uint16_t *w = p.w + ((int64_t)ex.e * p.n + c) * K + 8 * g;
+        const uint16_t *x[R];
+#pragma unroll
+        for (int i = 0; i < R; ++i)
+            x[i] = p.rows + (row0 + min(16 * i + r, valid - 1)) * K + 8 * g;
+        struct Block {
+            dev::bf16x8 w[2], x[R][2];
+        };
+        const auto fill = [&](Block &b, int kb) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const int32_t at = kb * 64 + h * 32;
+                b.w[h] = *reinterpret_cast<const dev::bf16x8 *>(w + at);
+#pragma unroll
+                for (int i = 0; i < R; ++i)
+                    b.x[i][h] = *reinterpret_cast<const dev::bf16x8 *>(x[i] + at);
+            }
+            __builtin_amdgcn_sched_barrier(0);
+        };
+        dev::f32x4 acc[R];
+#pragma unroll
+        for (int i = 0; i < R; ++i)
+            acc[i] = dev::f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+        const auto use = [&](const Block &b) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+                for (int i = 0; i < R; ++i)
+                    acc[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(b.w[h], b.x[i][h], acc[i], 0, 0, 0);
+            __builtin_amdgcn_sched_barrier(0);
+        };
+        if (wave < whole) {
+            // four blocks in flight; past the last one, the last one again
+            constexpr int S = kStripWaves;
+            const int count = (whole - wave + S - 1) / S, last = wave + (count - 1) * S;
+            Block b0, b1, b2, b3;
+            fill(b0, wave);
+            fill(b1, min(wave + S, last));
+            fill(b2, min(wave + 2 * S, last));
+            for (int i = 0; i < count; i += 4) {
+                const int kb = wave + i * S;
+                fill(b3, min(kb + 3 * S, last));
+                use(b0);
+                if (i + 1 >= count)
+                    break;
+                fill(b0, min(kb + 4 * S, last));
+                use(b1);
+                if (i + 2 >= count)
+                    break;
+                fill(b1, min(kb + 5 * S, last));
+                use(b2);
+                if (i + 3 >= count)
+                    break;
+                fill(b2, min(kb + 6 * S, last));
+                use(b3);
+            }
+        }
+        if (whole < KB && wave == whole % kStripWaves) {  // the rest: pieces of 8, zeros past the last
+            const dev::bf16x8 zero = {};
+            Block b;
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const int32_t at = whole * 64 + h * 32;
+                const bool inside = at + 8 * g < K;
+                b.w[h] = inside ? *reinterpret_cast<const dev::bf16x8 *>(w + at) : zero;
+#pragma unroll
+                for (int i = 0; i < R; ++i)
+                    b.x[i][h] = inside ? *reinterpret_cast<const dev::bf16x8 *>(x[i] + at) : zero;
+            }
+            use(b);
+        }
+#pragma unroll
+        for (int i = 0; i < R; ++i)
+            part[wave][i][lane] = acc[i];
+        __syncthreads();
+        if (wave < R) {  // a wave per 16 rows
+            dev::f32x4 v = part[0][wave][lane];
+#pragma unroll
+            for (int u = 1; u < kStripWaves; ++u)
+                v += part[u][wave][lane];
+            const int32_t row = 16 * wave + r;
+            const bool live = row < valid;
+            // channels 4 g .. of 16; gated: the upper lanes' are the up channels of the lower's
+            const int32_t at = P == kGated ? c0 + 4 * (g & 1) : c0 + 4 * g;
+            const bool inside = live && at < channels;
+            const auto pack = [](const dev::f32x4 &f) { return make_uint2(dev::pack_bf16(f[0], f[1]), dev::pack_bf16(f[2], f[3])); };
+            const auto unpack = [](const uint2 &u) {
+                return dev::f32x4{dev::bf16_lo(u.x), dev::bf16_hi(u.x), dev::bf16_lo(u.y), dev::bf16_hi(u.y)};
+            };
+            if (P == kLinear && p.bias != nullptr && inside)
+                v += unpack(*reinterpret_cast<const uint2 *>(p.bias + (int64_t)ex.e * p.n + at));
+            if (p.saved != nullptr && inside)
+                *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(p.saved) + (row0 + row) * p.n + at +
+                                           (P == kGated ? (g >> 1) * half : 0)) = pack(v);
+            dev::f32x4 up;
+            if constexpr (P == kGated) {
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    up[j] = __shfl_xor(v[j], 32);
+            }
+            dev::for_act(p.act, [&](auto act) {
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    v[j] = dev::act_value<decltype(act)::value>(v[j]);
+            });
+            uint16_t *y = p.y + (row0 + row) * channels + at;
+            if constexpr (P == kGated) {
+                v *= up;
+                if (inside && g < 2)
+                    *reinterpret_cast<uint2 *>(y) = pack(v);
+            } else if (inside) {
+                if (p.residual != nullptr)
+                    v += unpack(*reinterpret_cast<const uint2 *>(p.residual + (row0 + row) * p.n + at));
+                *reinterpret_cast<uint2 *>(y) = pack(v);
+            }
+        }
+        __syncthreads();  // part is rewritten by the next strip
+    }
+}
+
 // Row tiles of `rows` rows that a call can have: a segment's last one is partial.
 int64_t max_tiles(const TrainGemmArgs &p, int32_t rows)
 {
@@ -491,7 +647,7 @@ template <TrainProduct P, typename S>
 hipError_t launch_tiles(const TrainGemmArgs &p, hipStream_t stream)
 {
     const int32_t channels = P == kGated ? p.n / 2 : P == kGradInput ? p.k : p.n;
-    const int32_t width = P == kGated ? kTileN / 2 : kTileN;
+    const int32_t width = P == kGated ? S::BN / 2 : S::BN;
     const int32_t n_tiles = (channels + width - 1) / width;
     const int64_t tiles = max_tiles(p, S::BM) * n_tiles;
     // one block per compute unit (its stages fill LDS), a multiple of the 8 XCDs
@@ -501,10 +657,58 @@ hipError_t launch_tiles(const TrainGemmArgs &p, hipStream_t stream)
     return hipGetLastError();
 }
 
+template <TrainProduct P, int R>
+hipError_t launch_strips(const TrainGemmArgs &p, hipStream_t stream)
+{
+    const int32_t strips = P == kGated ? p.n / 16 : (p.n + 15) / 16;
+    const int64_t work = max_tiles(p, 16 * R) * strips, most = 8 * (int64_t)device_cu_count();
+    hipLaunchKernelGGL((train_gemm_strips<P, R>), dim3((uint32_t)(work < most ? work : most)), dim3(kStripWaves * kWave), 0,
+                       stream, p, strips);
+    return hipGetLastError();
+}
+
+// Row tiles that evenly routed experts have, about: half of them end in one more.
+int64_t likely_tiles(const TrainGemmArgs &p, int32_t rows)
+{
+    if (p.recv_count == nullptr)
+        return (p.max_rows + rows - 1) / rows;
+    const int64_t used = p.max_rows < p.E ? p.max_rows : p.E;
+    const int64_t tiles = p.max_rows / rows + p.E / 2;
+    return tiles < used ? used : tiles;
+}
+
 template <TrainProduct P>
 hipError_t launch_product(const TrainGemmArgs &p, hipStream_t stream)
 {
-    if (p.max_rows / p.E >= 512)
+    const int64_t cus = device_cu_count();
+    if constexpr (P != kGradInput) {
+        // Strips while four blocks per compute unit hold them all (in a graph, tiles /
+        // strips): one row, 7168 -> 4096 (256 strips) 58.7 / 13.6 us, 2048 -> 7168 (448) 20.5 /
+        // 10.7, 512 -> 512 9.0 / 4.9; 64 rows, 7168 -> 4096 (1024) 55 / 40, 2048 -> 7168
+        // (1792) 20 / 35; 128 rows, 2048 -> 2048 (1024) 26 / 18, 2048 -> 7168 (3584) 26 / 69.
+        // A block holds the rows of one expert, up to 64.  8-bit saved rows need the
+        // 128 channels of a block together, which strips do not have.
+        const int32_t strips = P == kGated ? p.n / 16 : (p.n + 15) / 16;
+        const bool quantized = p.saved != nullptr && p.saved_quant != MOE_QUANT_NONE;
+        const int64_t rows = (p.max_rows + p.E - 1) / p.E;
+        if (!quantized && max_tiles(p, 16) * strips <= 4 * cus) {
+            if (rows <= 16)
+                return launch_strips<P, 1>(p, stream);
+            if (rows <= 32)
+                return launch_strips<P, 2>(p, stream);
+            return launch_strips<P, 4>(p, stream);
+        }
+    }
+    // 256-row tiles need half as many rounds over the compute units, each of 1.6 times
+    // the time.  128 / 256 rows per tile: 4096 dense rows, 2048 -> 2048 (1 / 1 rounds) 34 /
+    // 55 us; 1111, 2056 -> 7184 (2 / 1) 69 / 63; 16 experts x 512 rows, 2048 -> 2048 (3 / 2)
+    // 82 / 109; 32 experts, 7168 -> 4096, 704 rows (12 / 7) 1396 / 1199, 512 (9 / 5) 1001 /
+    // 979; 256 rows, 2048 -> 7168 (9 / 6) 319 / 371.
+    const int32_t channels = P == kGated ? p.n / 2 : P == kGradInput ? p.k : p.n, width = P == kGated ? 128 : 256;
+    const int64_t n_tiles = (channels + width - 1) / width;
+    const int64_t rounds128 = (likely_tiles(p, 128) * n_tiles + cus - 1) / cus;
+    const int64_t rounds256 = (likely_tiles(p, 256) * n_tiles + cus - 1) / cus;
+    if (8 * rounds256 <= 5 * rounds128)
         return launch_tiles<P, Rows256>(p, stream);
     return launch_tiles<P, Rows128>(p, stream);
 }

@@ -15,19 +15,17 @@ namespace moe {
 namespace tile {
 namespace train {
 
-constexpr int kTileN = 256;  // output channels per block
-
-// A block's tile: BM rows x 256 channels on WR x WC waves of MT x NF fragments,
-// STEP summed channels a stage, STAGES stages in LDS.
-template <int BM_, int WR_, int WC_, int STEP_, int STAGES_>
+// A block's tile: BM rows x BN channels on WR x WC waves of MT x NF fragments, STEP
+// summed channels a stage, STAGES stages in LDS.
+template <int BM_, int BN_, int WR_, int WC_, int STEP_, int STAGES_>
 struct TileShape {
-    static constexpr int BM = BM_, WR = WR_, WC = WC_, kStep = STEP_, kStages = STAGES_;
+    static constexpr int BM = BM_, BN = BN_, WR = WR_, WC = WC_, kStep = STEP_, kStages = STAGES_;
     static constexpr int kWaves = WR * WC, kThreads = kWaves * kWave;
-    static constexpr int MT = BM / 16 / WR, NF = kTileN / 16 / WC;
+    static constexpr int MT = BM / 16 / WR, NF = BN / 16 / WC;
     static constexpr int kHalves = kStep / 32;                    // matrix instructions deep
     static constexpr int kRow = kStep * 2;                        // bytes of a row
-    static constexpr int kW = BM * kRow, kBytes = kW + kTileN * kRow;  // a stage: rows, then channels
-    static constexpr int kA = kW / 1024 / kWaves, kB = kTileN * kRow / 1024 / kWaves;  // a wave's loads of a stage
+    static constexpr int kW = BM * kRow, kBytes = kW + BN * kRow;  // a stage: rows, then channels
+    static constexpr int kA = kW / 1024 / kWaves, kB = BN * kRow / 1024 / kWaves;  // a wave's loads of a stage
     static constexpr int kLoads = kA + kB;
 };
 

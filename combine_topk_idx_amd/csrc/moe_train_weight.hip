@@ -16,8 +16,8 @@ namespace {
 using namespace tile;
 using namespace tile::train;
 
-using S = TileShape<128, 2, 2, 32, 3>;  // its rows are channels of dy
-constexpr int kTileM = S::BM;  // channels of dy per block
+using S = TileShape<128, 256, 2, 2, 32, 3>;  // its rows are channels of dy
+constexpr int kTileM = S::BM, kTileN = S::BN;  // channels of dy, and of a, per block
 constexpr int MT = S::MT, NF = S::NF, kStep = S::kStep, kHalf = S::kW;
 
 constexpr int kGroupM = 16;
