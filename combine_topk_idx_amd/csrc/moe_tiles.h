@@ -26,6 +26,15 @@ __device__ __forceinline__ int32_t scalar(int32_t v)
     return __builtin_amdgcn_readfirstlane(v);
 }
 
+// This lane's number, anew: what is computed from it stays with the code that uses
+// it.  Kept over a loop of tiles instead, it fills registers that the tiles need, is
+// spilled, and each reload waits for every store before it.
+__device__ __forceinline__ int here(int lane)
+{
+    asm volatile("" : "+v"(lane));
+    return lane;
+}
+
 // Word i (uniform) of an array that the kernel does not write, by a scalar load:
 // a vector load would wait for every load before it, whole stages of a tile.
 __device__ __forceinline__ int32_t word_of(const int32_t *a, int32_t i)

@@ -41,6 +41,7 @@ struct TileLoads {
     __device__ __forceinline__ void set(const TrainGemmArgs &p, const TileAt &at, int wave_, int lane)
     {
         wave = wave_;
+        lane = here(lane);
         K = depth<P>(p);
         const uint32_t row_bytes = (uint32_t)K * 2;
         const int row = Rows::row(wave, lane);
@@ -234,6 +235,7 @@ __device__ __forceinline__ void write_tile(const TrainGemmArgs &p, const dev::f3
 {
     constexpr int NF = S::NF;
     using B = SavedBlocks<P, S>;
+    lane = here(lane);
     const int g = lane >> 4;
     const int32_t channels = P == kGated ? p.n / 2 : P == kGradInput ? p.k : p.n;
     // this wave's channels (gated: of a half)
@@ -359,7 +361,7 @@ __device__ __forceinline__ void run_tile(const TrainGemmArgs &p, const TileAt &a
 {
     TileLoads<P, S> loads;
     loads.set(p, at, wave, lane);
-    const TileReads<P, S, MT> reads(wave, lane);
+    const TileReads<P, S, MT> reads(wave, here(lane));
     const int KB = scalar((loads.K + S::kStep - 1) / S::kStep);
     dev::f32x4 acc[S::NF][MT];
     clear(acc);

@@ -76,6 +76,7 @@ struct WeightLoads {
     __device__ __forceinline__ void set(const GradWeightArgs &p, const WeightTile &at, int wave_, int lane)
     {
         wave = wave_;
+        lane = here(lane);
         rows = at.rows;
         n = p.n;
         k = p.k;
@@ -174,6 +175,7 @@ __device__ __forceinline__ void write_weights(const GradWeightArgs &p, const dev
                                               const dev::f32x4 (&sums)[kBias], const WeightTile &at, int wr, int wc,
                                               int lane)
 {
+    lane = here(lane);
     const int32_t j0 = at.mt * kTileM, c0 = at.nt * kTileN + wc * NF * 16;
     const int32_t valid = min(kTileM, p.n - j0);
     const bool parts = p.splits > 1;
@@ -257,7 +259,7 @@ __device__ __forceinline__ void run_weights(const GradWeightArgs &p, const Weigh
     constexpr int kDma = k8 ? S::kA : S::kLoads, kStepLoads = k8 ? kDma + 8 : kDma;
     WeightLoads<QUANT> loads;
     loads.set(p, at, wave, lane);
-    const WeightReads reads(wave, lane);
+    const WeightReads reads(wave, here(lane));
     const int wr = wave / S::WC, wc = wave % S::WC;
     const int KB = scalar((at.rows + kStep - 1) / kStep);
     dev::f32x4 acc[NF][MT], sums[kBias];
