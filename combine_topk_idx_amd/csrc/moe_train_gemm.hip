@@ -391,10 +391,11 @@ __device__ __forceinline__ void run_tile(const TrainGemmArgs &p, const TileAt &a
         // halves the waves meet: the next stage is there and this one has been read, so
         // the step after next loads into it.
         Fragments<S, MT> first, second;
+        const auto none = [](auto) {};
         const auto step = [&](uint8_t *cur, uint8_t *other, int kb) {
-            multiply<false, S, MT>(acc, first, second, cur, 1, reads, loads, cur, 0);
+            multiply<false, S, MT>(acc, first, second, cur, 1, reads, loads, cur, 0, none);
             wait_and_meet<0>();
-            multiply<true, S, MT>(acc, second, first, other, 0, reads, loads, cur, kb + 2);
+            multiply<true, S, MT>(acc, second, first, other, 0, reads, loads, cur, kb + 2, none);
         };
         wait_and_meet<S::kLoads>();
         for_each<MT + S::NF>([&](auto N) { read_fragment<decltype(N)::value, S, MT>(first, st.s0, 0, reads); });

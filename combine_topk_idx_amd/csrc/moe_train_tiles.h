@@ -131,6 +131,14 @@ __device__ __forceinline__ void mfma_in_place(dev::f32x4 &acc, const dev::bf16x8
         : "v"(__builtin_bit_cast(dev::u32x4, w)), "v"(__builtin_bit_cast(dev::u32x4, x)));
 }
 
+// The same for a sum outside the accumulators, and w from anywhere.
+__device__ __forceinline__ void mfma_beside(dev::f32x4 &sum, const dev::bf16x8 &w, const dev::bf16x8 &x)
+{
+    asm("s_nop 1\n\tv_mfma_f32_16x16x32_bf16 %0, %1, %2, %0"
+        : "+v"(sum)
+        : "v"(__builtin_bit_cast(dev::u32x4, w)), "v"(__builtin_bit_cast(dev::u32x4, x)));
+}
+
 // The end of a loop of them: when it is the last turn (at >= end, uniform), the wait
 // before a sum is read or moved (at most 19 cycles).  It has to stand here, in one
 // piece with the loop: the compiler may move sums as soon as the loop is left.
@@ -146,11 +154,11 @@ __device__ __forceinline__ void end_turn(int at, int end)
 // into `next` and, with LOAD, step `kb_load` loads into the stage `free`.  One wave
 // has the SIMD: what is issued between two matrix instructions has to fit beside
 // one, so reads and loads stand one by one among them, the reads first (loads all
-// at once in the first half: 12% slower).
-template <bool LOAD, typename S, int MT, typename Reads, typename Loads>
+// at once in the first half: 12% slower).  extra(i): more to do after row fragment i.
+template <bool LOAD, typename S, int MT, typename Reads, typename Loads, typename Extra>
 __device__ __forceinline__ void multiply(dev::f32x4 (&acc)[S::NF][MT], const Fragments<S, MT> &now, Fragments<S, MT> &next,
                                          const uint8_t *st, int h, const Reads &reads, const Loads &loads, uint8_t *free,
-                                         int kb_load)
+                                         int kb_load, const Extra &extra)
 {
     constexpr int kAll = MT * S::NF, kReads = MT + S::NF, kGap = kAll / kReads > 3 ? 3 : kAll / kReads;
     for_each<kAll>([&](auto Q) {
@@ -160,6 +168,8 @@ __device__ __forceinline__ void multiply(dev::f32x4 (&acc)[S::NF][MT], const Fra
         if constexpr (LOAD)
             loads.template issue<q * S::kLoads / kAll, (q + 1) * S::kLoads / kAll>(free, kb_load);
         mfma_in_place(acc[f][i], now.w[f], now.x[i]);
+        if constexpr (f == S::NF - 1)
+            extra(std::integral_constant<int, i>());
         __builtin_amdgcn_sched_barrier(0);
     });
 }

@@ -2,7 +2,7 @@
 //
 //   dw[e, j, c] = sum over rows of e of dy[row, j] a[row, c],  dbias[e, j] = sum of dy[row, j]
 //
-// A block holds 128 x 256 of one expert's weights and walks its rows, 32 a step.
+// A block holds 256 x 256 (or 128 x 256) of one expert's weights and walks its rows, 32 a step.
 // Both operands are summed over their slow axis: the stages hold them as they lie
 // in memory and ds_read_b64_tr_b16 hands each lane four rows of one channel.
 // dbias comes from the same fragments, times ones.
@@ -16,11 +16,17 @@ namespace {
 using namespace tile;
 using namespace tile::train;
 
-using S = TileShape<128, 256, 2, 2, 32, 3>;  // its rows are channels of dy
-constexpr int kTileM = S::BM, kTileN = S::BN;  // channels of dy, and of a, per block
-constexpr int MT = S::MT, NF = S::NF, kStep = S::kStep, kHalf = S::kW;
+// A tile's rows are channels of dy, its channels a's.
+// Four waves, one per SIMD, each with 128 x 128; four stages.
+using Weights256 = TileShape<256, 256, 2, 2, 32, 4>;
+// Four waves with 64 x 128, two blocks per compute unit; three stages.
+using Weights128 = TileShape<128, 256, 2, 2, 32, 3>;
 
-constexpr int kGroupM = 16;
+// Tiles along dy's channels that walk a's together.  32 experts x 1024 rows, 4096 x 7168,
+// 256 x 256: 4 / 6 / 8 of them 1823 / 1812 / 1862 us; 128 x 256: 4 / 8 / 16 / 32 of them 2032 /
+// 2007 / 1988 / 2052.
+template <typename S>
+constexpr int group_tiles() { return S::BM == 256 ? 5 : 16; }
 
 struct WeightTile {
     int32_t e, split, mt, nt, rows;
@@ -61,16 +67,17 @@ struct Rows8<MOE_QUANT_NONE> {};
 
 // The loads of one tile.  Rows past the split's end lie past the buffers' ends and
 // are read as zeros, and so are channels past the last.
-template <int QUANT>
+template <typename S, int QUANT>
 struct WeightLoads {
-    using Dy = StepPlaces<kTileM>;
-    using A = StepPlaces<kTileN>;
+    static constexpr int kStep = S::kStep, kHalf = S::kW;
+    using Dy = StepPlaces<S::BM>;
+    using A = StepPlaces<S::BN>;
     static constexpr int kRowsPerPass = A::kSteps * S::kWaves;
     const uint16_t *dy;
     const uint8_t *a, *scale;
     uint32_t so, sstep, to;  // 8 bits: this lane's first scale, and its place in a stage
-    uint32_t yo, ao[2];     // this lane's place in its first rows
-    uint32_t ystep, astep;  // a pass of all waves further, two of a's (8 bits: one)
+    uint32_t yo[2], ao[2];  // this lane's place in its first rows
+    uint32_t ystep, astep;  // two passes of all waves further (a in 8 bits: one)
     int32_t rows, n, k, wave;
 
     __device__ __forceinline__ void set(const GradWeightArgs &p, const WeightTile &at, int wave_, int lane)
@@ -82,18 +89,18 @@ struct WeightLoads {
         k = p.k;
         dy = p.dy + at.row0 * n;
         a = static_cast<const uint8_t *>(p.a) + at.row0 * k * (QUANT == MOE_QUANT_NONE ? 2 : 1);
-        const int32_t j = at.mt * kTileM + Dy::channel(wave, lane);
-        yo = j < n ? (uint32_t)Dy::step(wave, lane) * (uint32_t)n * 2 + (uint32_t)j * 2 : 0x80000000u;
-        ystep = 2u * Dy::kSteps * S::kWaves * (uint32_t)n;
 #pragma unroll
         for (int odd = 0; odd < 2; ++odd) {  // passes by turns
-            const int32_t i = at.nt * kTileN + A::channel(wave + odd * S::kWaves, lane);
-            ao[odd] = i < k ? (uint32_t)A::step(wave + odd * S::kWaves, lane) * (uint32_t)k * 2 + (uint32_t)i * 2 : 0x80000000u;
+            const int u = wave + odd * S::kWaves;
+            const int32_t j = at.mt * S::BM + Dy::channel(u, lane), i = at.nt * S::BN + A::channel(u, lane);
+            yo[odd] = j < n ? (uint32_t)Dy::step(u, lane) * (uint32_t)n * 2 + (uint32_t)j * 2 : 0x80000000u;
+            ao[odd] = i < k ? (uint32_t)A::step(u, lane) * (uint32_t)k * 2 + (uint32_t)i * 2 : 0x80000000u;
         }
+        ystep = 4u * Dy::kSteps * S::kWaves * (uint32_t)n;
         astep = 4u * kRowsPerPass * (uint32_t)k;
         if constexpr (QUANT != MOE_QUANT_NONE) {
             const int s = A::step(wave, lane);
-            const int32_t piece = lane & 31, at_c = at.nt * kTileN + piece * 8;
+            const int32_t piece = lane & 31, at_c = at.nt * S::BN + piece * 8;
             ao[0] = at_c < k ? (uint32_t)s * (uint32_t)k + (uint32_t)at_c : 0x80000000u;
             astep = kRowsPerPass * (uint32_t)k;
             so = at_c < k ? (uint32_t)s * scale_bytes() + (uint32_t)(at_c / (QUANT == MOE_QUANT_MXFP8 ? 32 : 128)) *
@@ -129,7 +136,7 @@ struct WeightLoads {
         static_assert(kRowsPerPass == 8, "rows of a pass");
         *reinterpret_cast<dev::u32x4 *>(st + kHalf + (to ^ (i & 1) * 128) + i * kRowsPerPass * 512) = rows8.bf16(i);
     }
-    // Loads FROM .. TO - 1 of the 8 of step kb (8 bits: dy's 4).
+    // Loads FROM .. TO - 1 of step kb (8 bits: dy's).
     template <int FROM, int TO>
     __device__ __forceinline__ void issue(uint8_t *st, int kb) const
     {
@@ -139,7 +146,7 @@ struct WeightLoads {
             constexpr int j = FROM + decltype(N)::value, i = j < S::kA ? j : j - S::kA;
             if constexpr (j < S::kA)
                 load_lds<16>(buffer(dy + (int64_t)r0 * n, left * (uint32_t)n * 2), st + (wave + S::kWaves * i) * 1024,
-                             yo + i * ystep, 0);
+                             yo[i & 1] + (i >> 1) * ystep, 0);
             else if constexpr (QUANT == MOE_QUANT_NONE)
                 load_lds<16>(buffer(a + (int64_t)r0 * k * 2, left * (uint32_t)k * 2),
                              st + kHalf + (wave + S::kWaves * i) * 1024, ao[i & 1] + (i >> 1) * astep, 0);
@@ -147,37 +154,41 @@ struct WeightLoads {
     }
 };
 
+template <typename S>
 struct WeightReads {
     int row, column, m0, n0;
     __device__ __forceinline__ WeightReads(int wave, int lane)
     {
-        row = StepPlaces<kTileM>::read(lane);
-        column = StepPlaces<kTileN>::read(lane);
-        m0 = wave / S::WC * MT;
-        n0 = wave % S::WC * NF;
+        row = StepPlaces<S::BM>::read(lane);
+        column = StepPlaces<S::BN>::read(lane);
+        m0 = wave / S::WC * S::MT;
+        n0 = wave % S::WC * S::NF;
     }
     __device__ __forceinline__ dev::bf16x8 x(const uint8_t *st, int i, int) const
     {
-        return read_steps<kTileM>(st + (row ^ (m0 + i) * 32));
+        return read_steps<S::BM>(st + (row ^ (m0 + i) * 32));
     }
     __device__ __forceinline__ dev::bf16x8 w(const uint8_t *st, int f, int) const
     {
-        return read_steps<kTileN>(st + kHalf + (column ^ (n0 + f) * 32));
+        return read_steps<S::BN>(st + S::kW + (column ^ (n0 + f) * 32));
     }
 };
 
 // The waves that share a row of fragments share its sums for the bias.
-constexpr int kBias = MT / S::WC;
+template <typename S>
+constexpr int bias_sums() { return S::MT / S::WC; }
 
 // Results: channels 16 (MT wr + i) .. of dy, 16 (NF wc + f) .. of a.  Parts of a
 // split go to the workspace.
-__device__ __forceinline__ void write_weights(const GradWeightArgs &p, const dev::f32x4 (&acc)[NF][MT],
-                                              const dev::f32x4 (&sums)[kBias], const WeightTile &at, int wr, int wc,
-                                              int lane)
+template <typename S>
+__device__ __forceinline__ void write_weights(const GradWeightArgs &p, const dev::f32x4 (&acc)[S::NF][S::MT],
+                                              const dev::f32x4 (&sums)[bias_sums<S>()], const WeightTile &at, int wr,
+                                              int wc, int lane)
 {
+    constexpr int MT = S::MT, NF = S::NF;
     lane = here(lane);
-    const int32_t j0 = at.mt * kTileM, c0 = at.nt * kTileN + wc * NF * 16;
-    const int32_t valid = min(kTileM, p.n - j0);
+    const int32_t j0 = at.mt * S::BM, c0 = at.nt * S::BN + wc * NF * 16;
+    const int32_t valid = min(S::BM, p.n - j0);
     const bool parts = p.splits > 1;
     const int64_t group = parts ? (int64_t)at.e * p.splits + at.split : at.e;
     const int64_t first = (group * p.n + j0) * p.k;
@@ -216,8 +227,8 @@ __device__ __forceinline__ void write_weights(const GradWeightArgs &p, const dev
     if (p.dbias != nullptr && at.nt == 0 && g == 0) {
         float *out = parts ? p.partial + (int64_t)p.E * p.splits * p.n * p.k : p.dbias;
 #pragma unroll
-        for (int b = 0; b < kBias; ++b) {
-            const int row = (wr * MT + wc * kBias + b) * 16 + r;
+        for (int b = 0; b < bias_sums<S>(); ++b) {
+            const int row = (wr * MT + wc * bias_sums<S>() + b) * 16 + r;
             if (row < valid) {
                 float *to = out + group * p.n + j0 + row;
                 *to = !parts && p.accumulate ? *to + sums[b][0] : sums[b][0];
@@ -226,42 +237,58 @@ __device__ __forceinline__ void write_weights(const GradWeightArgs &p, const dev
     }
 }
 
-// The loads that a tile begins with: two stages, a in 8 bits through registers.
-template <int QUANT>
+// Sets of rows in 8 bits on their way.
+template <typename S>
+constexpr int rows8_sets() { return S::kStages == 4 ? 2 : 1; }
+
+// The loads that a tile begins with: four stages, or two of three; of a in 8 bits the
+// first one or two through registers.
+template <typename S, int QUANT>
 __device__ __forceinline__ void start_weights(const GradWeightArgs &p, const WeightTile &at, const Stages &st,
-                                              Rows8<QUANT> &rows8, int wave, int lane)
+                                              Rows8<QUANT> (&rows8)[rows8_sets<S>()], int wave, int lane)
 {
-    WeightLoads<QUANT> loads;
+    WeightLoads<S, QUANT> loads;
     loads.set(p, at, wave, lane);
     if constexpr (QUANT != MOE_QUANT_NONE) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-            loads.fetch(rows8, i, 0);
+        for (int u = 0; u < rows8_sets<S>(); ++u)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                loads.fetch(rows8[u], i, u);
         __builtin_amdgcn_sched_barrier(0);
     }
     loads.template issue<0, S::kLoads>(st.s0, 0);
     __builtin_amdgcn_sched_barrier(0);  // in this order: the waits count
     loads.template issue<0, S::kLoads>(st.s1, 1);
     __builtin_amdgcn_sched_barrier(0);
+    if constexpr (S::kStages == 4) {
+        loads.template issue<0, S::kLoads>(st.s2, 2);
+        __builtin_amdgcn_sched_barrier(0);
+        loads.template issue<0, S::kLoads>(st.s3, 3);
+        __builtin_amdgcn_sched_barrier(0);
+    }
 }
 
 // Multiplies a tile whose first loads are in flight, then starts the next tile's
 // (`more`) and writes the results.
 //
-// a in 8 bits goes through registers: rows fetched in step u are put into their
-// stage in step u + 1 and read in step u + 2.
-template <int QUANT, bool BIAS>
+// a in 8 bits goes through registers.  Four stages: rows fetched in step u are put into
+// their stage in step u + 2 and read in step u + 3; three: put in step u + 1, read in
+// step u + 2.  Loads come back in order, so waiting for them sooner would wait for dy's
+// too.
+template <typename S, int QUANT, bool BIAS>
 __device__ __forceinline__ void run_weights(const GradWeightArgs &p, const WeightTile &at, const WeightTile &next, bool more,
-                                            const Stages &st, Rows8<QUANT> &rows8, int wave, int lane)
+                                            const Stages &st, Rows8<QUANT> (&rows8)[rows8_sets<S>()], int wave, int lane)
 {
+    constexpr int MT = S::MT, NF = S::NF, kBias = bias_sums<S>();
     constexpr bool k8 = QUANT != MOE_QUANT_NONE;
     // a stage's loads that go to LDS, and the loads of a step
     constexpr int kDma = k8 ? S::kA : S::kLoads, kStepLoads = k8 ? kDma + 8 : kDma;
-    WeightLoads<QUANT> loads;
+    WeightLoads<S, QUANT> loads;
     loads.set(p, at, wave, lane);
-    const WeightReads reads(wave, here(lane));
+    const WeightReads<S> reads(wave, here(lane));
     const int wr = wave / S::WC, wc = wave % S::WC;
-    const int KB = scalar((at.rows + kStep - 1) / kStep);
+    const int KB = scalar((at.rows + S::kStep - 1) / S::kStep);
     dev::f32x4 acc[NF][MT], sums[kBias];
     clear(acc);
 #pragma unroll
@@ -269,49 +296,90 @@ __device__ __forceinline__ void run_weights(const GradWeightArgs &p, const Weigh
         sums[b] = dev::f32x4{0.0f, 0.0f, 0.0f, 0.0f};
     if constexpr (k8) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            loads.put(rows8, i, st.s0);
-            loads.fetch(rows8, i, 1);
-        }
+        for (int u = 0; u < rows8_sets<S>(); ++u)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                loads.put(rows8[u], i, u == 0 ? st.s0 : st.s1);
+                loads.fetch(rows8[u], i, rows8_sets<S>() + u);
+            }
         __builtin_amdgcn_sched_barrier(0);
     }
-    // cur: the stage of step kb, after: kb + 1, free: kb + 2
-    const auto step = [&](uint8_t *cur, uint8_t *after, uint8_t *free, int kb) {
-        wait_and_meet<kStepLoads>();
+    const auto add_bias = [&](const uint8_t *cur) {
         if constexpr (BIAS) {  // the waves of a row of fragments share its sums, read again
             const __bf16 one = (__bf16)1.0f;
             const dev::bf16x8 ones = {one, one, one, one, one, one, one, one};
 #pragma unroll
-            for (int b = 0; b < kBias; ++b)
-                sums[b] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(ones, reads.x(cur, wc * kBias + b, 0), sums[b], 0, 0, 0);
-        }
-        multiply_stage<S, MT>(acc, cur, reads, loads, free, kb + 2, [&](auto I) {
-            constexpr int i = decltype(I)::value;
-            if constexpr (k8) {
-                loads.put(rows8, i, after);
-                loads.fetch(rows8, i, kb + 2);
+            for (int b = 0; b < kBias; ++b) {
+                const dev::bf16x8 x = reads.x(cur, wc * kBias + b, 0);
+                if constexpr (S::kStages == 4)
+                    mfma_beside(sums[b], ones, x);  // the compiler would take accumulators for them
+                else
+                    sums[b] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(ones, x, sums[b], 0, 0, 0);
             }
-        });
+        }
     };
-    static_assert(MT == 4 && S::kHalves == 1, "a pass of a step's rows beside each row fragment");
     // Whole rounds: steps past the last multiply zeros.  Ways out between the steps would
     // have the sums change registers where they meet.
-    for (int kb = 0; kb < KB; kb += 3) {
-        step(st.s0, st.s1, st.s2, kb);
-        step(st.s1, st.s2, st.s0, kb + 1);
-        step(st.s2, st.s0, st.s1, kb + 2);
+    if constexpr (S::kStages == 4) {
+        static_assert(MT == 8 && S::kHalves == 1, "four passes of a step's rows: put, then fetched");
+        Fragments<S, MT> even, odd;
+        wait_and_meet<3 * kDma>();
+        for_each<MT + NF>([&](auto N) { read_fragment<decltype(N)::value, S, MT>(even, st.s0, 0, reads); });
+        // cur: the stage of step kb, after: kb + 1, put: kb + 2
+        const auto step = [&](Fragments<S, MT> &now, Fragments<S, MT> &then, Rows8<QUANT> &r8, uint8_t *cur, uint8_t *after,
+                              uint8_t *put, int kb) {
+            if constexpr (BIAS)
+                add_bias(cur);
+            wait_and_meet<2 * kStepLoads>();
+            multiply<true, S, MT>(acc, now, then, after, 0, reads, loads, cur, kb + 4, [&](auto I) {
+                constexpr int i = decltype(I)::value;
+                if constexpr (k8 && i < 4)
+                    loads.put(r8, i, put);
+                if constexpr (k8 && i >= 4)
+                    loads.fetch(r8, i - 4, kb + 4);
+            });
+        };
+        for (int kb = 0; kb < KB; kb += 4) {
+            step(even, odd, rows8[0], st.s0, st.s1, st.s2, kb);
+            step(odd, even, rows8[1], st.s1, st.s2, st.s3, kb + 1);
+            step(even, odd, rows8[0], st.s2, st.s3, st.s0, kb + 2);
+            step(odd, even, rows8[1], st.s3, st.s0, st.s1, kb + 3);
+            end_turn(kb + 4, KB);
+        }
+    } else {
+        static_assert(MT == 4 && S::kHalves == 1, "a pass of a step's rows beside each row fragment");
+        // cur: the stage of step kb, after: kb + 1, free: kb + 2
+        const auto step = [&](uint8_t *cur, uint8_t *after, uint8_t *free, int kb) {
+            wait_and_meet<kStepLoads>();
+            add_bias(cur);
+            multiply_stage<S, MT>(acc, cur, reads, loads, free, kb + 2, [&](auto I) {
+                constexpr int i = decltype(I)::value;
+                if constexpr (k8) {
+                    loads.put(rows8[0], i, after);
+                    loads.fetch(rows8[0], i, kb + 2);
+                }
+            });
+        };
+        for (int kb = 0; kb < KB; kb += 3) {
+            step(st.s0, st.s1, st.s2, kb);
+            step(st.s1, st.s2, st.s0, kb + 1);
+            step(st.s2, st.s0, st.s1, kb + 2);
+        }
     }
     wait_and_meet<0>();
     if (more)
-        start_weights<QUANT>(p, next, st, rows8, wave, lane);
-    write_weights(p, acc, sums, at, wr, wc, lane);
+        start_weights<S, QUANT>(p, next, st, rows8, wave, lane);
+    write_weights<S>(p, acc, sums, at, wr, wc, lane);
 }
 
-template <int QUANT>
-__global__ __launch_bounds__(S::kThreads, 2) void grad_weight_tiles(GradWeightArgs p, int32_t m_tiles, int32_t n_tiles)
+template <typename S, int QUANT>
+__global__ __launch_bounds__(S::kThreads, S::kStages == 4 ? 1 : 2) void grad_weight_tiles(GradWeightArgs p, int32_t m_tiles,
+                                                                                        int32_t n_tiles)
 {
+    constexpr int kStep = S::kStep, kGroupM = group_tiles<S>();
     __shared__ alignas(1024) uint8_t st0[S::kBytes], st1[S::kBytes], st2[S::kBytes];
-    const Stages st = {st0, st1, st2, nullptr};
+    __shared__ alignas(1024) uint8_t st3[S::kStages == 4 ? S::kBytes : 16];
+    const Stages st = {st0, st1, st2, st3};
     const int lane = threadIdx.x & (kWave - 1);
     const int wave = scalar(threadIdx.x / kWave);
     const int32_t tiles = m_tiles * n_tiles;
@@ -322,7 +390,6 @@ __global__ __launch_bounds__(S::kThreads, 2) void grad_weight_tiles(GradWeightAr
         const int32_t t = scalar((int32_t)(work - (int64_t)part * tiles));
         at.e = scalar(part / p.splits);
         at.split = scalar(part - at.e * p.splits);
-        // groups of kGroupM tiles along dy's channels walk a's together
         const int32_t grp = scalar(t / (kGroupM * n_tiles)), in_grp = scalar(t - grp * kGroupM * n_tiles);
         const int32_t wide = min(kGroupM, m_tiles - grp * kGroupM);
         at.nt = scalar(in_grp / wide);
@@ -343,9 +410,9 @@ __global__ __launch_bounds__(S::kThreads, 2) void grad_weight_tiles(GradWeightAr
     int64_t idx = blockIdx.x >> 3;
     if (idx >= end)
         return;
-    Rows8<QUANT> rows8;
+    Rows8<QUANT> rows8[rows8_sets<S>()];
     WeightTile next = locate(base + idx);
-    start_weights<QUANT>(p, next, st, rows8, wave, lane);
+    start_weights<S, QUANT>(p, next, st, rows8, wave, lane);
     for (;;) {
         const WeightTile at = next;
         idx += gridDim.x >> 3;
@@ -353,9 +420,9 @@ __global__ __launch_bounds__(S::kThreads, 2) void grad_weight_tiles(GradWeightAr
         if (more)
             next = locate(base + idx);
         if (p.dbias != nullptr && at.nt == 0)
-            run_weights<QUANT, true>(p, at, next, more, st, rows8, wave, lane);
+            run_weights<S, QUANT, true>(p, at, next, more, st, rows8, wave, lane);
         else
-            run_weights<QUANT, false>(p, at, next, more, st, rows8, wave, lane);
+            run_weights<S, QUANT, false>(p, at, next, more, st, rows8, wave, lane);
         if (!more)
             break;
     }
@@ -384,39 +451,57 @@ __global__ __launch_bounds__(kBlockThreads) void grad_weight_join(GradWeightArgs
     *to = p.accumulate ? *to + v : v;
 }
 
+int64_t weight_tiles(int32_t E, int32_t n, int32_t k, int32_t rows)
+{
+    return (int64_t)E * ((n + rows - 1) / rows) * ((k + 255) / 256);
+}
+
+// 256 x 256 from half the compute units on: two smaller blocks on each hide each other's
+// waits, but read a half more.  128 / 256: 8191 rows, 768 x 2048 (24 tiles of 256) 40 / 51
+// us; 32,768 rows, 4096 x 7168 (448) 1658 / 1391; 32 experts x 1024 rows 1975 / 1812.
+bool wide_weights(int32_t E, int32_t n, int32_t k) { return weight_tiles(E, n, k, 256) >= 128; }
+
+template <typename S>
+hipError_t launch_weights(const GradWeightArgs &p, hipStream_t stream)
+{
+    const int32_t m_tiles = (p.n + S::BM - 1) / S::BM, n_tiles = (p.k + S::BN - 1) / S::BN;
+    const int64_t work = (int64_t)m_tiles * n_tiles * p.E * p.splits;
+    // the blocks that compute units hold (LDS), a multiple of the 8 XCDs
+    const int64_t most = ((S::kStages == 4 ? 1 : 2) * device_cu_count() + 7) / 8 * 8;
+    const dim3 grid((uint32_t)(work < most ? (work + 7) / 8 * 8 : most)), block(S::kThreads);
+    switch (p.a_quant) {
+    case MOE_QUANT_FP8_F32:
+        hipLaunchKernelGGL((grad_weight_tiles<S, MOE_QUANT_FP8_F32>), grid, block, 0, stream, p, m_tiles, n_tiles);
+        break;
+    case MOE_QUANT_FP8_UE8M0:
+        hipLaunchKernelGGL((grad_weight_tiles<S, MOE_QUANT_FP8_UE8M0>), grid, block, 0, stream, p, m_tiles, n_tiles);
+        break;
+    case MOE_QUANT_MXFP8:
+        hipLaunchKernelGGL((grad_weight_tiles<S, MOE_QUANT_MXFP8>), grid, block, 0, stream, p, m_tiles, n_tiles);
+        break;
+    default:
+        hipLaunchKernelGGL((grad_weight_tiles<S, MOE_QUANT_NONE>), grid, block, 0, stream, p, m_tiles, n_tiles);
+    }
+    return hipGetLastError();
+}
+
 }  // namespace
 
 int32_t grad_weight_splits(int64_t max_rows, int32_t E, int32_t n, int32_t k)
 {
+    if (wide_weights(E, n, k))
+        return 1;
     // 256 blocks, one per compute unit, of at least 512 rows: more of them write and read
     // more parts (8191 rows, 768 x 2048, 48 tiles: 256 / 384 / 512 blocks 42 / 45 / 48 us;
     // 2048 x 2048, 128 tiles: 81 / 93 / 88)
-    const int64_t tiles = (int64_t)E * ((n + kTileM - 1) / kTileM) * ((k + kTileN - 1) / kTileN);
-    const int64_t most = max_rows / E / 512, splits = 256 / tiles;
+    const int64_t most = max_rows / E / 512, splits = 256 / weight_tiles(E, n, k, 128);
     return (int32_t)(splits < 1 || most < 1 ? 1 : splits < most ? splits : most);
 }
 
 hipError_t launch_grad_weight(const GradWeightArgs &p, hipStream_t stream)
 {
-    const int32_t m_tiles = (p.n + kTileM - 1) / kTileM, n_tiles = (p.k + kTileN - 1) / kTileN;
-    const int64_t work = (int64_t)m_tiles * n_tiles * p.E * p.splits;
-    // one block per compute unit (its stages fill LDS), a multiple of the 8 XCDs
-    const int64_t cus = (2 * device_cu_count() + 7) / 8 * 8;
-    const dim3 grid((uint32_t)(work < cus ? (work + 7) / 8 * 8 : cus)), block(S::kThreads);
-    switch (p.a_quant) {
-    case MOE_QUANT_FP8_F32:
-        hipLaunchKernelGGL((grad_weight_tiles<MOE_QUANT_FP8_F32>), grid, block, 0, stream, p, m_tiles, n_tiles);
-        break;
-    case MOE_QUANT_FP8_UE8M0:
-        hipLaunchKernelGGL((grad_weight_tiles<MOE_QUANT_FP8_UE8M0>), grid, block, 0, stream, p, m_tiles, n_tiles);
-        break;
-    case MOE_QUANT_MXFP8:
-        hipLaunchKernelGGL((grad_weight_tiles<MOE_QUANT_MXFP8>), grid, block, 0, stream, p, m_tiles, n_tiles);
-        break;
-    default:
-        hipLaunchKernelGGL((grad_weight_tiles<MOE_QUANT_NONE>), grid, block, 0, stream, p, m_tiles, n_tiles);
-    }
-    hipError_t e = hipGetLastError();
+    const hipError_t e = wide_weights(p.E, p.n, p.k) ? launch_weights<Weights256>(p, stream)
+                                                     : launch_weights<Weights128>(p, stream);
     if (e != hipSuccess || p.splits == 1)
         return e;
     const int64_t quads = (int64_t)p.E * p.n * p.k / 4, all = quads + (p.dbias != nullptr ? (int64_t)p.E * p.n / 4 : 0);

@@ -137,6 +137,8 @@ LAYOUTS = {
     "masked": dict(T=64, E=4, K=2, layout="masked", capacity=21, seed=3),            # drops pairs
     "many": dict(T=700, E=2, K=2, layout="contiguous", align=128, holes=0.1, seed=4),
     "none": dict(T=9, E=3, K=1, layout="contiguous", align=4, holes=1.0, seed=5),    # no pair at all
+    "wide": dict(T=150, E=130, K=3, layout="contiguous", align=1, holes=0.1, seed=6),   # few rows of many experts
+    "wide_long": dict(T=500, E=129, K=2, layout="contiguous", align=8, used=3, seed=7),  # many rows of few
 }
 
 
@@ -388,6 +390,18 @@ def _grad_weight_reference(rows, dy, q, s, quant):
     ("many", 328, 264, BF16, torch.float32, True),
     ("many", 64, 384, MX, torch.float32, False),
     ("none", 64, 128, FP8, torch.bfloat16, True),
+    # 128 tiles of weights and more: 256 x 256 each
+    ("wide", 24, 72, BF16, torch.float32, True),
+    ("wide", 264, 40, BF16, torch.bfloat16, True),
+    ("wide", 40, 128, FP8, torch.float32, True),
+    ("wide_long", 328, 264, BF16, torch.float32, False),
+    ("wide_long", 136, 328, BF16, torch.bfloat16, True),
+    ("wide_long", 264, 384, FP8, torch.bfloat16, True),
+    ("wide_long", 72, 640, UE8M0, torch.float32, True),
+    ("wide_long", 264, 256, MX, torch.bfloat16, True),
+    ("dense300", 2048, 4096, BF16, torch.float32, True),
+    ("dense", 4096, 2048, MX, torch.bfloat16, True),
+    ("one", 2056, 4104, BF16, torch.float32, True),
 ])
 def test_grad_weight(layout, n, k, quant, dtype, bias):
     _say(f"grad weight {layout} n={n} k={k} quant={quant} {dtype} bias={bias}")
@@ -410,7 +424,8 @@ def test_grad_weight(layout, n, k, quant, dtype, bias):
         _untouched(db[rows.E], "dbias behind the last expert")
 
 
-@pytest.mark.parametrize("layout,n,k", [("dense", 72, 136), ("dense700", 264, 256), ("packed", 40, 264), ("none", 8, 64)])
+@pytest.mark.parametrize("layout,n,k", [("dense", 72, 136), ("dense700", 264, 256), ("packed", 40, 264), ("none", 8, 64),
+                                        ("wide", 40, 264), ("wide_long", 264, 72)])
 def test_grad_weight_accumulates(layout, n, k):
     _say(f"grad weight accumulates {layout} n={n} k={k}")
     rows = Rows(**LAYOUTS[layout])

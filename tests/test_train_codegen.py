@@ -16,14 +16,15 @@ from combine_topk_idx_amd import build as B
 
 OPTIONS = ["--offload-arch=gfx950", "-O3", "-std=c++17", "-fPIC", "-ffp-contract=off", "-Xclang", "-target-feature",
            "-Xclang", "-packed-fp32-ops", "-I", os.path.join(B.ROOT, "include"), "-I", os.path.join(B.PKG, "csrc")]
+FILES = ["moe_train_gemm.hip", "moe_train_weight.hip"]
 
 
-@pytest.fixture(scope="module")
-def kernels(tmp_path_factory):
-    """(name, {label: instructions} in order) of the kernels that hold sums in accumulators."""
+@pytest.fixture(scope="module", params=FILES)
+def kernels(request, tmp_path_factory):
+    """(name, {label: instructions} in order) of a file's kernels that hold sums in accumulators."""
     out = str(tmp_path_factory.mktemp("s") / "k.s")
     subprocess.run([B.hipcc(), *OPTIONS, "-S", "--cuda-device-only", "-o", out,
-                    os.path.join(B.PKG, "csrc", "moe_train_gemm.hip")], check=True, capture_output=True, timeout=600)
+                    os.path.join(B.PKG, "csrc", request.param)], check=True, capture_output=True, timeout=600)
     found = []
     for m in re.finditer(r"^(_ZN\S+):\s*;.*?\n(.*?)\.Lfunc_end", open(out).read(), re.S | re.M):
         if not re.search(r"v_mfma\S+ a\[", m[2]):
