@@ -25,8 +25,9 @@ template <TrainProduct P>
 __device__ __forceinline__ int32_t depth(const TrainGemmArgs &p) { return P == kGradInput ? p.n : p.k; }
 
 // The loads of one tile: descriptors (uniform) and this lane's offsets.  Rows
-// past the tile's end are read as its last row and channels past the last as that
-// one (the gradient's: as zeros); what comes of the copies is not stored.  Summed
+// past the tile's end are zeros, which spare their loads and the matrix units' power
+// (4096 unequal rows over 32 experts: 0.7% against copies of the last row); channels past
+// the last are read as that one (the gradient's: as zeros).  Neither is stored.  Summed
 // channels past the last are zeros in both operands: bit 31 of an offset takes it
 // past its buffer's end, which the range check turns into zeros.
 template <TrainProduct P, typename S>
@@ -49,7 +50,7 @@ struct TileLoads {
         a = buffer(p.rows + at.row0 * K, (uint32_t)at.valid * row_bytes);
 #pragma unroll
         for (int i = 0; i < S::kA; ++i)
-            ao[i] = (uint32_t)min(row + Rows::kPass * i, at.valid - 1) * row_bytes + piece * 2;
+            ao[i] = row + Rows::kPass * i < at.valid ? (uint32_t)(row + Rows::kPass * i) * row_bytes + piece * 2 : 0x80000000u;
         if constexpr (P == kGradInput) {
             stride = p.k;
 #pragma unroll
