@@ -131,7 +131,7 @@ LAYOUTS = {
     "one": dict(T=1),
     "dense": dict(T=67),
     "dense300": dict(T=300),
-    "dense700": dict(T=700),                                   # 256-row tiles
+    "dense700": dict(T=700),
     "contiguous": dict(T=41, E=5, K=2, layout="contiguous", align=16, holes=0.2, seed=1),
     "packed": dict(T=90, E=7, K=3, layout="contiguous", align=1, used=4, seed=2),    # experts without rows
     "masked": dict(T=64, E=4, K=2, layout="masked", capacity=21, seed=3),            # drops pairs
@@ -139,6 +139,13 @@ LAYOUTS = {
     "none": dict(T=9, E=3, K=1, layout="contiguous", align=4, holes=1.0, seed=5),    # no pair at all
     "wide": dict(T=150, E=130, K=3, layout="contiguous", align=1, holes=0.1, seed=6),   # few rows of many experts
     "wide_long": dict(T=500, E=129, K=2, layout="contiguous", align=8, used=3, seed=7),  # many rows of few
+    # with thousands of channels: 256-row tiles, whose last one is nearly full, half full, a quarter full, one row
+    "dense250": dict(T=250),
+    "dense340": dict(T=340),
+    "dense310": dict(T=310),
+    "dense257": dict(T=257),
+    "experts": dict(T=300, E=5, K=2, layout="contiguous", align=1, holes=0.1, seed=8),
+    "slab": dict(T=260, E=3, K=2, layout="masked", capacity=200, used=2, seed=9),
 }
 
 
@@ -175,6 +182,19 @@ def _run_gated(rows, k, inter, kind, save, seed):
     ("many", 136, 384, M.ACT_SILU, MX),
     ("many", 128, 264, M.ACT_GELU, None),
     ("none", 64, 128, M.ACT_SILU, FP8),
+    # strips of one expert's rows: 16, 32 and 64 rows
+    ("wide", 200, 24, M.ACT_SILU, None),
+    ("contiguous", 1096, 24, M.ACT_SILU, BF16),
+    ("packed", 584, 40, M.ACT_GELU, BF16),
+    # 256-row tiles; one step, odd and even numbers of steps, steps that end early; two rounds over the chip
+    ("dense250", 64, 16520, M.ACT_SILU, BF16),
+    ("dense250", 328, 49280, M.ACT_SILU, None),
+    ("dense340", 8, 12800, M.ACT_GELU, UE8M0),
+    ("dense310", 136, 12680, M.ACT_SILU, None),
+    ("dense257", 192, 12800, M.ACT_SILU, MX),
+    ("experts", 200, 5632, M.ACT_RELU, FP8),
+    ("experts", 72, 19720, M.ACT_SILU, BF16),
+    ("slab", 392, 8448, M.ACT_SILU, UE8M0),
 ])
 def test_gated(layout, k, inter, kind, save):
     _say(f"gated {layout} k={k} inter={inter} act={kind} save={save}")
@@ -212,6 +232,21 @@ def test_gated(layout, k, inter, kind, save):
     ("many", 264, 128, M.ACT_RELU, True, True, UE8M0),
     ("many", 64, 1000, M.ACT_NONE, True, False, BF16),
     ("none", 64, 64, M.ACT_NONE, True, True, None),
+    # strips of one expert's rows: 16, 32 and 64 rows
+    ("wide", 136, 40, M.ACT_GELU, True, True, BF16),
+    ("wide", 2120, 8, M.ACT_NONE, True, False, None),
+    ("contiguous", 1544, 72, M.ACT_GELU, True, True, BF16),
+    ("packed", 584, 24, M.ACT_SILU, True, True, BF16),
+    ("masked", 264, 136, M.ACT_RELU, False, True, None),
+    # 256-row tiles; one step, odd and even numbers of steps, steps that end early; two rounds over the chip
+    ("dense250", 40, 33032, M.ACT_NONE, True, True, BF16),
+    ("dense250", 256, 98560, M.ACT_SILU, True, False, None),
+    ("dense340", 136, 25608, M.ACT_GELU, True, True, None),
+    ("dense310", 200, 25600, M.ACT_SILU, True, True, UE8M0),
+    ("dense257", 72, 25600, M.ACT_NONE, True, False, MX),
+    ("experts", 392, 11264, M.ACT_GELU, True, True, FP8),
+    ("experts", 64, 39432, M.ACT_RELU, True, True, BF16),
+    ("slab", 128, 16904, M.ACT_NONE, True, True, None),
 ])
 def test_linear(layout, k, n, kind, bias, residual, save):
     _say(f"linear {layout} k={k} n={n} act={kind} bias={bias} residual={residual} save={save}")
@@ -342,6 +377,9 @@ def test_activation_backward_far_values(kind):
     ("dense", 72, 24), ("dense", 64, 256), ("dense", 520, 264),
     ("dense300", 136, 520), ("dense700", 200, 264), ("dense700", 1024, 72),
     ("contiguous", 40, 1000), ("packed", 328, 128), ("masked", 128, 8), ("many", 72, 512), ("none", 64, 64),
+    # 256-row tiles; one step, odd and even numbers of steps, steps that end early; two rounds over the chip
+    ("dense250", 40, 33032), ("dense250", 136, 98560), ("dense340", 264, 25608), ("dense310", 64, 25600),
+    ("dense257", 192, 25600), ("experts", 200, 11272), ("experts", 328, 39432), ("slab", 72, 16904),
 ])
 def test_grad_input(layout, n, k):
     _say(f"grad input {layout} n={n} k={k}")
