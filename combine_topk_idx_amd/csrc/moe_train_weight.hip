@@ -447,7 +447,8 @@ __global__ __launch_bounds__(kBlockThreads) void grad_weight_join(GradWeightArgs
             make_uint2(dev::pack_bf16(v[0], v[1]), dev::pack_bf16(v[2], v[3]));
         return;
     }
-    dev::f32x4 *to = reinterpret_cast<dev::f32x4 *>((bias ? p.dbias : static_cast<float *>(p.dw)) + i);
+    using Quad = float __attribute__((ext_vector_type(4), aligned(4)));  // dbias has a float's alignment
+    Quad *to = reinterpret_cast<Quad *>((bias ? p.dbias : static_cast<float *>(p.dw)) + i);
     *to = p.accumulate ? *to + v : v;
 }
 

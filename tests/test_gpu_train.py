@@ -502,6 +502,26 @@ def test_grad_weight_splits_rows(T, bias):
         _untouched(dw[1], "dw")
 
 
+@pytest.mark.parametrize("quant,accumulate", [(BF16, False), (BF16, True), (FP8, True), (UE8M0, False), (MX, True)])
+def test_grad_weight_splits_rows_of_experts(quant, accumulate):
+    """Rows shared by several blocks for each of three experts, one of them without rows; dbias with a float's alignment."""
+    _say(f"grad weight splits experts' rows quant={quant} accumulate={accumulate}")
+    T, n, k = 1700, 72, 256
+    rows = Rows(T, E=3, K=2, layout="contiguous", align=16, used=2, holes=0.1, seed=31)
+    g = _gen(T)
+    dy = rows.input(g, n)
+    q, s = rows.formatted(g, k, quant)
+    assert M.moe_grad_weight_workspace_bytes(rows.cfg, T, n, k) > 0
+    dw, db = torch.randn(4, n, k, generator=g, device="cuda"), torch.randn(3 * n + 2, generator=g, device="cuda")
+    was, bwas = dw.clone(), db.clone()
+    _grad_weight(rows, n, k, dy, q, s, quant, dw, db[1:-1].view(3, n), accumulate)
+    assert torch.equal(dw[3], was[3]) and torch.equal(db[[0, -1]], bwas[[0, -1]])
+    for e, (v, b), (sv, sb) in _grad_weight_reference(rows, dy, q, s, quant):
+        old, bold = was[e].to(D) * accumulate, bwas[1:-1].view(3, n)[e].to(D) * accumulate
+        R.assert_near(dw[e], old + v, b + (old.abs() + v.abs()) * 2.0 ** -23, "dw")
+        R.assert_near(db[1:-1].view(3, n)[e], bold + sv, sb + (bold.abs() + sv.abs()) * 2.0 ** -23, "dbias")
+
+
 def test_grad_weight_of_no_tokens():
     """An empty batch has gradients of zero, or leaves sums as they are."""
     _say("grad weight of no tokens")
@@ -772,6 +792,84 @@ def test_rows_do_not_mix(T):
     assert not bool(nan.any())
     dw[0][e, [5, 130]], dw[1][e, [5, 130]] = 0.0, 0.0
     assert torch.equal(*dw)
+
+
+@pytest.mark.parametrize("T", [3, 600])
+@pytest.mark.parametrize("save", [FP8, UE8M0, MX])
+def test_saved_rows_do_not_mix(T, save):
+    """A row with a NaN is saved as NaN in 8 bits, and no other row shows it."""
+    _say(f"saved rows do not mix T={T} save={save}")
+    rows = Rows(T, H=136, E=3, K=2, layout="contiguous", align=8, seed=9)
+    g = _gen(T)
+    a, w = rows.input(g, 136), _weights(g, 3, 512, 136)
+    lo, hi = next(s for s in rows.spans if s[1] - s[0] > 1)
+    bad = lo + (hi - lo) // 2
+    got = []
+    for i in range(2):
+        if i:
+            a[bad, 5] = float("nan")
+        y, h = _filled((rows.n, 512), torch.bfloat16), _filled((rows.n, 256), torch.bfloat16)
+        (q, s), (gq, gs) = _format_buffers(rows.n, 512, save), _format_buffers(rows.n, 512, save)
+        M.moe_expert_linear(rows.cfg, T, 512, 136, M.ACT_SILU, a, w, None, None, rows.handle, y, q, s, save)
+        M.moe_ffn_gated(rows.cfg, T, 256, M.ACT_SILU, a, w, rows.handle, h, gq, gs, save)
+        got.append([y, h, q, s, gq, gs])
+    torch.cuda.synchronize()
+    keep = torch.arange(rows.n, device="cuda") != bad
+    for was, now in zip(*got):
+        assert torch.equal(was[keep].view(torch.uint8), now[keep].view(torch.uint8))
+    y, h, q, _, gq, _ = got[1]
+    assert bool(y[bad].isnan().all()) and bool(h[bad].isnan().all())
+    assert bool(((q[bad] & 0x7F) == 0x7F).all()) and bool(((gq[bad] & 0x7F) == 0x7F).all())
+
+
+# ---- many experts -------------------------------------------------------------------------
+
+
+def test_most_experts():
+    """2048 experts of a few rows each, and the most choices of a token."""
+    _say("2048 experts")
+    T, E, K, k, n = 90, 2048, 32, 72, 128
+    rows = Rows(T, H=k, E=E, K=K, layout="contiguous", align=4, holes=0.1, seed=41)
+    g = _gen(41)
+    a, w, dy = rows.input(g, k), _weights(g, E, n, k), rows.input(g, n)
+    y, z = _filled((rows.n + 2, n), torch.bfloat16), _filled((rows.n + 2, n), torch.bfloat16)
+    h, da = _filled((rows.n + 2, n // 2), torch.bfloat16), _filled((rows.n + 2, k), torch.bfloat16)
+    q, s = _format_buffers(rows.n + 2, n, UE8M0)
+    dw, db = _filled((E, n, k), torch.float32), _filled((E, n), torch.float32)
+    M.moe_expert_linear(rows.cfg, T, n, k, M.ACT_NONE, a, w, None, None, rows.handle, y)
+    M.moe_expert_linear(rows.cfg, T, n, k, M.ACT_NONE, a, w, None, None, rows.handle, z, q, s, UE8M0)
+    M.moe_ffn_gated(rows.cfg, T, n // 2, M.ACT_SILU, a, w, rows.handle, h)
+    M.moe_expert_grad_input(rows.cfg, T, n, k, dy, w, rows.handle, da)
+    _grad_weight(rows, n, k, dy, a, None, BF16, dw, db)
+    expert = torch.full((rows.n,), -1, device="cuda")
+    for e, (lo, hi) in enumerate(rows.spans):
+        expert[lo:hi] = e
+    at = torch.nonzero(expert >= 0).squeeze(1)
+    of = expert[at]
+    for e0 in range(0, E, 512):  # 64-bit weights of a share of the experts
+        some = at[(of >= e0) & (of < e0 + 512)]
+        we = w[expert[some]].to(D)
+        x, d = a[some].to(D), dy[some].to(D)
+        p = (we * x.unsqueeze(1)).sum(2)
+        b = (k + 8) * 2.0 ** -23 * (we * x.unsqueeze(1)).abs().sum(2)
+        R.assert_bf16(y[some], p, b, "y")
+        R.assert_bf16(z[some], p, b, "y beside saved rows")
+        R.assert_rows(q[some], s[some], p, b, UE8M0, "saved")
+        v, bv = R.gated(p, b, R.SILU)
+        R.assert_bf16(h[some], v, bv, "h")
+        v = (we * d.unsqueeze(2)).sum(1)
+        R.assert_bf16(da[some], v, (n + 8) * 2.0 ** -23 * (we * d.unsqueeze(2)).abs().sum(1), "da")
+        want, bound = torch.zeros(512, n, k, dtype=D, device="cuda"), torch.zeros(512, n, k, dtype=D, device="cuda")
+        terms = d.unsqueeze(2) * x.unsqueeze(1)
+        want.index_add_(0, expert[some] - e0, terms)
+        bound.index_add_(0, expert[some] - e0, terms.abs())
+        R.assert_near(dw[e0:e0 + 512], want, bound * (T + 8) * 2.0 ** -23, "dw")
+        bias, size = torch.zeros(512, n, dtype=D, device="cuda"), torch.zeros(512, n, dtype=D, device="cuda")
+        bias.index_add_(0, expert[some] - e0, d)
+        size.index_add_(0, expert[some] - e0, d.abs())
+        R.assert_near(db[e0:e0 + 512], bias, size * (T + 8) * 2.0 ** -23, "dbias")
+    for t, what in ((y, "y"), (z, "y beside saved rows"), (q, "saved"), (s, "scales"), (h, "h"), (da, "da")):
+        rows.check_untouched(t, what)
 
 
 # ---- offsets past 32 bits -----------------------------------------------------------------
