@@ -146,6 +146,7 @@ struct SavedBlocks {
     static constexpr int kHalves = P == kGated ? 2 : 1;       // gate and up, or all channels
     static constexpr int kOwn = S::NF / kHalves;              // fragments of a half, per wave
     static constexpr int kShare = kQuantGroup / (kOwn * 16);  // waves of a block
+    static constexpr bool kWhole = kShare <= S::WC;           // a tile has whole blocks
 };
 
 // Largest magnitude of a row's channels in COUNT fragments of a wave.
@@ -279,8 +280,8 @@ __device__ __forceinline__ void write_tile(const TrainGemmArgs &p, const dev::f3
                 v[f] += add[f];
         });
     };
-    const bool quantized = P != kGradInput && p.saved != nullptr && p.saved_quant != MOE_QUANT_NONE;
-    if constexpr (P != kGradInput && B::kShare > 1) {
+    const bool quantized = P != kGradInput && B::kWhole && p.saved != nullptr && p.saved_quant != MOE_QUANT_NONE;
+    if constexpr (P != kGradInput && B::kWhole && B::kShare > 1) {
         if (quantized && p.saved_quant != MOE_QUANT_MXFP8) {
             for_each<MT>([&](auto I) {
                 dev::f32x4 v[NF];
@@ -301,14 +302,15 @@ __device__ __forceinline__ void write_tile(const TrainGemmArgs &p, const dev::f3
         dev::f32x4 v[NF];
         row_sums(I, v);
         if constexpr (P != kGradInput) {
-            if (quantized) {
-                if (p.saved_quant == MOE_QUANT_FP8_F32)
+            if constexpr (B::kWhole) {
+                if (quantized && p.saved_quant == MOE_QUANT_FP8_F32)
                     save_quantized<P, MOE_QUANT_FP8_F32, S>(p, v, at, row0, wc, lane, wave_max);
-                else if (p.saved_quant == MOE_QUANT_FP8_UE8M0)
+                else if (quantized && p.saved_quant == MOE_QUANT_FP8_UE8M0)
                     save_quantized<P, MOE_QUANT_FP8_UE8M0, S>(p, v, at, row0, wc, lane, wave_max);
-                else
+                else if (quantized)
                     save_quantized<P, MOE_QUANT_MXFP8, S>(p, v, at, row0, wc, lane, wave_max);
-            } else if (p.saved != nullptr) {
+            }
+            if (!quantized && p.saved != nullptr) {
                 store_fragments<B::kOwn>(saved, v, row0, c0, lane);
                 if constexpr (P == kGated) {
                     Lines up = saved;
@@ -351,6 +353,12 @@ using Rows128 = TileShape<128, 256, 2, 4, 64, 3>;
 // matrix instruction fall to two thirds of what eight waves of 128 x 64 need, which
 // together with the loads' writes would keep LDS as busy as the matrix cores.
 using Rows256 = TileShape<256, 256, 2, 2, 64, 2>;
+// 64 rows and 128 channels: four waves, three stages, two blocks per compute unit.  Four
+// times the blocks of 128 x 256, for calls too small to fill the chip with those: a step
+// takes 0.35 us instead of 0.75, mostly latency.
+using Rows64 = TileShape<64, 128, 2, 2, 64, 3>;
+template <typename S>
+constexpr int blocks_per_cu() { return S::BM == 64 ? 2 : 1; }  // what LDS holds of their stages
 
 // Starts the loads of a tile's first two stages.
 template <TrainProduct P, typename S>
@@ -425,7 +433,7 @@ __device__ __forceinline__ void run_tile(const TrainGemmArgs &p, const TileAt &a
 }
 
 template <TrainProduct P, typename S>
-__global__ __launch_bounds__(S::kThreads, 1) void train_gemm_tiles(TrainGemmArgs p, int32_t n_tiles)
+__global__ __launch_bounds__(S::kThreads, blocks_per_cu<S>()) void train_gemm_tiles(TrainGemmArgs p, int32_t n_tiles)
 {
     constexpr int BM = S::BM;
     __shared__ int32_t tile_start[kMaxExperts / kGroup + 1];
@@ -485,9 +493,9 @@ __global__ __launch_bounds__(S::kThreads, 1) void train_gemm_tiles(TrainGemmArgs
         constexpr int MT = S::MT, kWide = 16 * S::WR;
         if (at.valid > MT / 2 * kWide)
             run_tile<P, S, MT>(p, at, next, more, st, wave_max, wave, lane);
-        else if (at.valid > MT / 4 * kWide)
+        else if (MT == 2 || at.valid > MT / 4 * kWide)
             run_tile<P, S, MT / 2>(p, at, next, more, st, wave_max, wave, lane);
-        else
+        else if constexpr (MT > 2)
             run_tile<P, S, MT / 4>(p, at, next, more, st, wave_max, wave, lane);
         if (!more)
             break;
@@ -666,7 +674,7 @@ hipError_t launch_tiles(const TrainGemmArgs &p, hipStream_t stream)
     const int32_t n_tiles = (channels + width - 1) / width;
     const int64_t tiles = max_tiles(p, S::BM) * n_tiles;
     // one block per compute unit (its stages fill LDS), a multiple of the 8 XCDs
-    const int64_t cus = (device_cu_count() + 7) / 8 * 8;
+    const int64_t cus = (blocks_per_cu<S>() * device_cu_count() + 7) / 8 * 8;
     const int64_t grid = tiles < cus ? (tiles + 7) / 8 * 8 : cus;
     hipLaunchKernelGGL((train_gemm_tiles<P, S>), dim3((uint32_t)grid), dim3(S::kThreads), 0, stream, p, n_tiles);
     return hipGetLastError();
@@ -696,34 +704,39 @@ template <TrainProduct P>
 hipError_t launch_product(const TrainGemmArgs &p, hipStream_t stream)
 {
     const int64_t cus = device_cu_count();
+    const bool quantized = p.saved != nullptr && p.saved_quant != MOE_QUANT_NONE;
     if constexpr (P != kGradInput) {
-        // Strips while four blocks per compute unit hold them all (in a graph, tiles /
-        // strips): one row, 7168 -> 4096 (256 strips) 58.7 / 13.6 us, 2048 -> 7168 (448) 20.5 /
-        // 10.7, 512 -> 512 9.0 / 4.9; 64 rows, 7168 -> 4096 (1024) 55 / 40, 2048 -> 7168
-        // (1792) 20 / 35; 128 rows, 2048 -> 2048 (1024) 26 / 18, 2048 -> 7168 (3584) 26 / 69.
-        // A block holds the rows of one expert, up to 64.  8-bit saved rows need the
-        // 128 channels of a block together, which strips do not have.
+        // Strips for up to 32 rows per expert, while three blocks per compute unit hold them
+        // all (in a graph, 64-row tiles / strips): one row, 7168 -> 4096 (256 strips) 38 / 13.6
+        // us, 2048 -> 7168 (448) 14.7 / 11.0; 16 rows, 512 -> 512 (32) 7.0 / 6.1; 32 rows, 7168 ->
+        // 4096 (512) 38 / 26, 2048 -> 2048 (256) 14.7 / 12.0; 64 rows, 2048 -> 2048 (512) 12.6 /
+        // 18.3; 8 experts, 2048 -> 1024, 2 rows each (576) 15.4 / 12.7, 16 rows (1024) 15.5 /
+        // 23.8.  8-bit saved rows need the 128 channels of a block together, which strips do not
+        // have.
         const int32_t strips = P == kGated ? p.n / 16 : (p.n + 15) / 16;
-        const bool quantized = p.saved != nullptr && p.saved_quant != MOE_QUANT_NONE;
         const int64_t rows = (p.max_rows + p.E - 1) / p.E;
-        if (!quantized && max_tiles(p, 16) * strips <= 4 * cus) {
-            if (rows <= 16)
-                return launch_strips<P, 1>(p, stream);
-            if (rows <= 32)
-                return launch_strips<P, 2>(p, stream);
-            return launch_strips<P, 4>(p, stream);
-        }
+        if (!quantized && rows <= 32 && max_tiles(p, 16) * strips <= 3 * cus)
+            return rows <= 16 ? launch_strips<P, 1>(p, stream) : launch_strips<P, 2>(p, stream);
     }
+    const int32_t channels = P == kGated ? p.n / 2 : P == kGradInput ? p.k : p.n;
+    const auto rounds = [&](int32_t rows, int32_t width) {  // over the compute units
+        return (likely_tiles(p, rows) * ((channels + width - 1) / width) + cus - 1) / cus;
+    };
+    const int64_t rounds128 = rounds(128, P == kGated ? 128 : 256);
+    // 64-row tiles, one per compute unit, take half the time of 128-row tiles with twice the
+    // channels, two as long: 128 / 64 rows per tile: 128 dense rows, 2048 -> 2048 (32 tiles of
+    // 64 rows) 25.7 / 12.6 us; 2048 rows, 1024 -> 1024 (256) 17.4 / 9.9, 2048 -> 2048 (512) 27.9 /
+    // 25.6; 8 experts x 256 rows, 2048 -> 2048 (576) 29.3 / 34.0; 32 experts x 128 rows, 512 ->
+    // 1536 (960, against two rounds) 28.9 / 19.7; 4096 dense rows, 2048 -> 2048 (1024) 37 / 50.
+    // A gated one of them has 64 of the 128 channels of an 8-bit block.
+    if (!(P == kGated && quantized) && rounds(64, P == kGated ? 64 : 128) <= 2 * rounds128)
+        return launch_tiles<P, Rows64>(p, stream);
     // 256-row tiles need half as many rounds over the compute units, each of 1.6 times
     // the time.  128 / 256 rows per tile: 4096 dense rows, 2048 -> 2048 (1 / 1 rounds) 34 /
     // 55 us; 1111, 2056 -> 7184 (2 / 1) 69 / 63; 16 experts x 512 rows, 2048 -> 2048 (3 / 2)
     // 82 / 109; 32 experts, 7168 -> 4096, 704 rows (12 / 7) 1396 / 1199, 512 (9 / 5) 1001 /
     // 979; 256 rows, 2048 -> 7168 (9 / 6) 319 / 371.
-    const int32_t channels = P == kGated ? p.n / 2 : P == kGradInput ? p.k : p.n, width = P == kGated ? 128 : 256;
-    const int64_t n_tiles = (channels + width - 1) / width;
-    const int64_t rounds128 = (likely_tiles(p, 128) * n_tiles + cus - 1) / cus;
-    const int64_t rounds256 = (likely_tiles(p, 256) * n_tiles + cus - 1) / cus;
-    if (8 * rounds256 <= 5 * rounds128)
+    if (8 * rounds(256, P == kGated ? 128 : 256) <= 5 * rounds128)
         return launch_tiles<P, Rows256>(p, stream);
     return launch_tiles<P, Rows128>(p, stream);
 }

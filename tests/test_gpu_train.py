@@ -194,7 +194,14 @@ def _run_gated(rows, k, inter, kind, save, seed):
     ("dense257", 192, 12800, M.ACT_SILU, MX),
     ("experts", 200, 5632, M.ACT_RELU, FP8),
     ("experts", 72, 19720, M.ACT_SILU, BF16),
+    ("dense310", 72, 13640, M.ACT_SILU, BF16),
     ("slab", 392, 8448, M.ACT_SILU, UE8M0),
+    # 128-row tiles; the last one nearly full, half full, a quarter full
+    ("dense", 72, 16456, M.ACT_GELU, BF16),
+    ("dense300", 200, 6728, M.ACT_SILU, BF16),
+    ("dense257", 64, 6728, M.ACT_RELU, None),
+    ("experts", 392, 3080, M.ACT_SILU, BF16),
+    ("slab", 136, 4360, M.ACT_GELU, None),
 ])
 def test_gated(layout, k, inter, kind, save):
     _say(f"gated {layout} k={k} inter={inter} act={kind} save={save}")
@@ -246,7 +253,18 @@ def test_gated(layout, k, inter, kind, save):
     ("dense257", 72, 25600, M.ACT_NONE, True, False, MX),
     ("experts", 392, 11264, M.ACT_GELU, True, True, FP8),
     ("experts", 64, 39432, M.ACT_RELU, True, True, BF16),
+    ("dense310", 136, 27144, M.ACT_NONE, True, True, None),
     ("slab", 128, 16904, M.ACT_NONE, True, True, None),
+    # 128-row tiles; the last one nearly full, half full, a quarter full
+    ("dense", 136, 32904, M.ACT_SILU, True, True, BF16),
+    ("dense300", 72, 13448, M.ACT_GELU, True, True, None),
+    ("dense257", 264, 13440, M.ACT_SILU, True, True, UE8M0),
+    ("experts", 64, 6152, M.ACT_NONE, True, True, BF16),
+    ("experts", 200, 6144, M.ACT_GELU, True, False, MX),
+    ("slab", 392, 8712, M.ACT_RELU, False, True, None),
+    # 64-row tiles past the first round
+    ("dense700", 136, 4104, M.ACT_GELU, True, True, BF16),
+    ("many", 72, 3080, M.ACT_SILU, True, True, None),
 ])
 def test_linear(layout, k, n, kind, bias, residual, save):
     _say(f"linear {layout} k={k} n={n} act={kind} bias={bias} residual={residual} save={save}")
@@ -379,7 +397,11 @@ def test_activation_backward_far_values(kind):
     ("contiguous", 40, 1000), ("packed", 328, 128), ("masked", 128, 8), ("many", 72, 512), ("none", 64, 64),
     # 256-row tiles; one step, odd and even numbers of steps, steps that end early; two rounds over the chip
     ("dense250", 40, 33032), ("dense250", 136, 98560), ("dense340", 264, 25608), ("dense310", 64, 25600),
-    ("dense257", 192, 25600), ("experts", 200, 11272), ("experts", 328, 39432), ("slab", 72, 16904),
+    ("dense257", 192, 25600), ("experts", 200, 11272), ("experts", 328, 39432), ("slab", 72, 16904), ("dense310", 200, 27144),
+    # 128-row tiles; the last one nearly full, half full, a quarter full
+    ("dense", 136, 32904), ("dense300", 72, 13448), ("dense257", 264, 13440), ("experts", 64, 6152), ("slab", 392, 8712),
+    # 64-row tiles past the first round
+    ("dense700", 136, 4104), ("many", 72, 3080),
 ])
 def test_grad_input(layout, n, k):
     _say(f"grad input {layout} n={n} k={k}")
