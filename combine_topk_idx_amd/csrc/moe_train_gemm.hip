@@ -357,8 +357,11 @@ using Rows256 = TileShape<256, 256, 2, 2, 64, 2>;
 // times the blocks of 128 x 256, for calls too small to fill the chip with those: a step
 // takes 0.35 us instead of 0.75, mostly latency.
 using Rows64 = TileShape<64, 128, 2, 2, 64, 3>;
+// The same for gated products saved in 8 bits, which need the 128 channels of a block of
+// both halves.
+using Wide64 = TileShape<64, 256, 2, 2, 64, 3>;
 template <typename S>
-constexpr int blocks_per_cu() { return S::BM == 64 ? 2 : 1; }  // what LDS holds of their stages
+constexpr int blocks_per_cu() { return S::BM == 64 && S::BN == 128 ? 2 : 1; }  // what LDS holds of their stages
 
 // Starts the loads of a tile's first two stages.
 template <TrainProduct P, typename S>
@@ -728,9 +731,15 @@ hipError_t launch_product(const TrainGemmArgs &p, hipStream_t stream)
     // 64 rows) 25.7 / 12.6 us; 2048 rows, 1024 -> 1024 (256) 17.4 / 9.9, 2048 -> 2048 (512) 27.9 /
     // 25.6; 8 experts x 256 rows, 2048 -> 2048 (576) 29.3 / 34.0; 32 experts x 128 rows, 512 ->
     // 1536 (960, against two rounds) 28.9 / 19.7; 4096 dense rows, 2048 -> 2048 (1024) 37 / 50.
-    // A gated one of them has 64 of the 128 channels of an 8-bit block.
     if (!(P == kGated && quantized) && rounds(64, P == kGated ? 64 : 128) <= 2 * rounds128)
         return launch_tiles<P, Rows64>(p, stream);
+    // As wide as the others, one per compute unit: not where a call has no more of them (8-bit
+    // rows of fp32 scales, 128 / 64 rows per tile: 64 rows, 7168 -> 4096 58 / 63 us; 512 rows 79 /
+    // 64; 512 rows, 2048 -> 2048 31.0 / 24.3, 4096 rows (512 tiles) 42 / 54; 32 experts x 128
+    // rows, 512 -> 1536 43 / 27).
+    if constexpr (P == kGated)
+        if (quantized && likely_tiles(p, 64) > likely_tiles(p, 128) && rounds(64, 128) <= rounds128)
+            return launch_tiles<P, Wide64>(p, stream);
     // 256-row tiles need half as many rounds over the compute units, each of 1.6 times
     // the time.  128 / 256 rows per tile: 4096 dense rows, 2048 -> 2048 (1 / 1 rounds) 34 /
     // 55 us; 1111, 2056 -> 7184 (2 / 1) 69 / 63; 16 experts x 512 rows, 2048 -> 2048 (3 / 2)

@@ -196,6 +196,11 @@ def _run_gated(rows, k, inter, kind, save, seed):
     ("experts", 72, 19720, M.ACT_SILU, BF16),
     ("dense310", 72, 13640, M.ACT_SILU, BF16),
     ("slab", 392, 8448, M.ACT_SILU, UE8M0),
+    # 64-row tiles, 256 channels wide, and wider than one round of them: 128 rows
+    ("dense257", 136, 384, M.ACT_SILU, UE8M0),
+    ("masked", 328, 256, M.ACT_GELU, FP8),
+    ("dense", 64, 17024, M.ACT_SILU, MX),
+    ("dense300", 72, 7296, M.ACT_SILU, UE8M0),
     # 128-row tiles; the last one nearly full, half full, a quarter full
     ("dense", 72, 16456, M.ACT_GELU, BF16),
     ("dense300", 200, 6728, M.ACT_SILU, BF16),
