@@ -21,13 +21,14 @@ FILES = ["moe_train_gemm.hip", "moe_train_weight.hip"]
 
 @pytest.fixture(scope="module", params=FILES)
 def kernels(request, tmp_path_factory):
-    """(name, {label: instructions} in order) of a file's kernels that hold sums in accumulators."""
+    """(name, {label: instructions} in order) of a file's kernels that multiply in inline assembly
+    (in others the compiler, which may use accumulators too, knows of every wait)."""
     out = str(tmp_path_factory.mktemp("s") / "k.s")
     subprocess.run([B.hipcc(), *OPTIONS, "-S", "--cuda-device-only", "-o", out,
                     os.path.join(B.PKG, "csrc", request.param)], check=True, capture_output=True, timeout=600)
     found = []
     for m in re.finditer(r"^(_ZN\S+):\s*;.*?\n(.*?)\.Lfunc_end", open(out).read(), re.S | re.M):
-        if not re.search(r"v_mfma\S+ a\[", m[2]):
+        if not re.search(r"#ASMSTART\s+v_mfma\S+ a\[", m[2]):
             continue
         blocks, label = {"entry": []}, "entry"
         for line in m[2].split("\n"):
