@@ -13,7 +13,7 @@
 // Bound by the matrix cores at the clock that the chip's power allows: 32,768 dense rows,
 // 7168 -> 2 x 2048 gated 1396 us (1380 TFLOP/s), gradient 1389; 8192^3 719 us gated, 741
 // linear, 735 gradient (1484 to 1530 TFLOP/s).  32 experts with 900 to 1150 rows each take
-// 1680 us (with 8-bit saved rows 1770 to 1800): a ninth row of tiles on some compute units
+// 1680 us (with 8-bit saved rows 1770 to 1830): a ninth row of tiles on some compute units
 // where the mean is 8.3, weights that 32 experts do not share, results that nothing overlaps.
 // Few rows are bound by the weights' bytes: 128 tokens x 8 over 64 experts, 2048 -> 7168 337
 // us (5.6 TB/s).  No LDS bank conflicts in any of them.
