@@ -258,7 +258,8 @@ moe_status_t moe_combine_backward(const moe_config_t *cfg, int32_t num_tokens, c
         return st;
     if ((st = check_handle(handle)) != MOE_OK)
         return st;
-    if ((st = check_tokens(*cfg, num_tokens)) != MOE_OK || num_tokens == 0)
+    if ((st = check_tokens(*cfg, num_tokens)) != MOE_OK || (st = check_channels(cfg->hidden)) != MOE_OK ||
+        num_tokens == 0)
         return st;
     if (!pointer(dout, 16) || !pointer(topk_w, 4) || !pointer(dy, 16) || !aligned(y, 16) || !aligned(dtopk_w, 4) ||
         (y == nullptr) != (dtopk_w == nullptr))
