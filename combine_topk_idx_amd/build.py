@@ -16,6 +16,10 @@ PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 LIB = os.path.join(PKG, "libmoe_dispatch.so")
 ARCH = "gfx950"
+OPTIONS = [f"--offload-arch={ARCH}", "-O3", "-std=c++17", "-fPIC", "-ffp-contract=off",
+           # packed-fp32 VALU forms stay off: plain fp32 code only
+           "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",
+           "-I", os.path.join(ROOT, "include"), "-I", os.path.join(PKG, "csrc")]
 
 
 def hipcc() -> str:
@@ -27,11 +31,7 @@ def hipcc() -> str:
 def build(verbose: bool = False) -> str:
     srcs = sorted(glob.glob(os.path.join(PKG, "csrc", "*.hip")))
     tmp = LIB + ".tmp"
-    cmd = [hipcc(), f"--offload-arch={ARCH}", "-O3", "-std=c++17", "-fPIC", "-shared",
-           "-ffp-contract=off",
-           # packed-fp32 VALU forms stay off: plain fp32 code only
-           "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",
-           "-Wall", "-I", os.path.join(ROOT, "include"), "-I", os.path.join(PKG, "csrc"),
+    cmd = [hipcc(), *OPTIONS, "-shared", "-Wall",
            "-o", tmp, *srcs]
     if verbose:
         print(" ".join(cmd), flush=True)
