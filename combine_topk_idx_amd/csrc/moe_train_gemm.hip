@@ -390,7 +390,7 @@ __device__ __forceinline__ void run_tile(const TrainGemmArgs &p, const TileAt &a
     if constexpr (S::kStages == 3) {
         const auto step = [&](uint8_t *cur, uint8_t *free, int kb) {
             wait_and_meet<S::kLoads>();
-            multiply_stage<S, MT>(acc, cur, reads, loads, free, kb + 2, [](auto) {});
+            multiply_stage<S, MT>(acc, cur, reads, loads, free, kb + 2, [](auto, const auto &) {});
         };
         // The first steps stand before the loop: there the compiler's own waits allow
         // for the stores of the tile before, in the loop they would hold up each turn.

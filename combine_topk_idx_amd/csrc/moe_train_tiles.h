@@ -175,8 +175,8 @@ __device__ __forceinline__ void multiply(dev::f32x4 (&acc)[S::NF][MT], const Fra
 }
 
 // acc += the stage `st`, two waves per SIMD: fragments are read as they are needed,
-// while step `kb_load` loads into the stage `free`.  extra(i): more to do after row
-// fragment i.
+// while step `kb_load` loads into the stage `free`.  extra(i, x): more to do after row
+// fragment i, whose halves are x.
 template <typename S, int MT, typename Reads, typename Loads, typename Extra>
 __device__ __forceinline__ void multiply_stage(dev::f32x4 (&acc)[S::NF][MT], const uint8_t *st, const Reads &reads,
                                                const Loads &loads, uint8_t *free, int kb_load, const Extra &extra)
@@ -197,7 +197,7 @@ __device__ __forceinline__ void multiply_stage(dev::f32x4 (&acc)[S::NF][MT], con
             constexpr int h = decltype(Q)::value / S::NF, f = decltype(Q)::value % S::NF;
             acc[f][i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w[f][h], x[i & 1][h], acc[f][i], 0, 0, 0);
         });
-        extra(I);
+        extra(I, x[i & 1]);
         loads.template issue<i * S::kLoads / MT, (i + 1) * S::kLoads / MT>(free, kb_load);
         __builtin_amdgcn_sched_barrier(0);
     });

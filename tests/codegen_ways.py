@@ -150,3 +150,54 @@ def hazards(kernel):
                 if to not in todo:
                     todo.append(to)
     return sorted(found)
+
+
+def loops(kernel):
+    """The innermost loops that multiply, as lists of their blocks' (first, last) positions: what leads back to a
+    block that every way to it passes."""
+    code, labels, _ = kernel
+    starts = blocks_of(code, labels)
+    ends = dict(zip(starts, starts[1:] + [len(code)]))
+    to = {b: sorted({p for p, _ in _ways(code, labels, b, ends[b]) if p < len(code)}) for b in starts}
+    order, seen, stack = [], {0}, [(0, iter(to[0]))]  # blocks, each after those it leads to
+    while stack:
+        b, rest = stack[-1]
+        nxt = next((p for p in rest if p not in seen), None)
+        if nxt is None:
+            order.append(b)
+            stack.pop()
+        else:
+            seen.add(nxt)
+            stack.append((nxt, iter(to[nxt])))
+    order.reverse()
+    number = {b: i for i, b in enumerate(order)}
+    ahead = {b: [] for b in order}
+    for b in order:
+        for p in to[b]:
+            ahead[p].append(b)
+    every = (1 << len(order)) - 1
+    passed = {b: every for b in order}  # as bits: the blocks on every way to one
+    passed[0] = 1
+    changed = True
+    while changed:
+        changed = False
+        for b in order[1:]:
+            bits = every
+            for p in ahead[b]:
+                bits &= passed[p]
+            bits |= 1 << number[b]
+            changed |= bits != passed[b]
+            passed[b] = bits
+    bodies = {}
+    for b in order:
+        for head in to[b]:
+            if passed[b] >> number[head] & 1:
+                body, todo = bodies.setdefault(head, {head}), [b]
+                while todo:
+                    x = todo.pop()
+                    if x not in body:
+                        body.add(x)
+                        todo += ahead[x]
+    found = [body for body in bodies.values()
+             if sum(code[i].startswith("v_mfma") for b in body for i in range(b, ends[b])) >= 16]
+    return [[(b, ends[b] - 1) for b in sorted(body)] for body in found if not any(o < body for o in found)]

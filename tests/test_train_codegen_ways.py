@@ -1,8 +1,9 @@
 """The compiled code of the bf16 products along every way through it (no GPU
-needed): sums in accumulators and in vector registers, operands, and what starts
-a sum.  codegen_ways has the rules; mistakes are planted in small pieces of code
-to show that they are found."""
+needed): sums in accumulators and in vector registers, operands, what starts a
+sum, and loops that stay free of spilled registers.  codegen_ways has the rules;
+mistakes are planted in small pieces of code to show that they are found."""
 import os
+import re
 import subprocess
 
 import pytest
@@ -47,6 +48,31 @@ def test_no_hazard_on_any_way(kernels):
         inline += sum(kernel[0][i].startswith("v_mfma") for i in kernel[2])
         assert not W.hazards(kernel), name
     assert inline > 3000
+
+
+def test_loops_that_multiply_do_not_spill(kernels):
+    """No scratch access in a tile's loop, and no wait for every load but the kernels' own: a reload waits for all loads
+    before it, whole stages that the loop's counted waits leave on their way."""
+    seen = 0
+    for name, kernel in kernels.items():
+        if "tiles" not in name:
+            continue
+        inner = W.loops(kernel)
+        assert inner, name
+        for blocks in inner:
+            seen += 1
+            for first, last in blocks:
+                idle = False  # no load since a wait for all of them
+                for i in range(first, last + 1):
+                    x = kernel[0][i]
+                    assert not x.startswith("scratch_"), f"{name}: {x}"
+                    if re.match(r"s_waitcnt .*vmcnt\(0\)", x):
+                        own = "lgkmcnt(0)" in x and kernel[0][i + 1].startswith("s_barrier")
+                        assert own or idle, f"{name}: {x}"
+                        idle = True
+                    elif x.startswith(("buffer_", "global_")):
+                        idle = False
+    assert seen >= 40
 
 
 # ---- mistakes that have to be found ------------------------------------------------------------
