@@ -246,6 +246,7 @@ moe_status_t moe_expert_grad_weight(const moe_config_t *cfg, int32_t num_tokens,
     p.n = n;
     p.k = k;
     p.dense_rows = num_tokens;
+    p.max_rows = rows;
     return from_hip(launch_grad_weight(p, static_cast<hipStream_t>(stream)));
 }
 

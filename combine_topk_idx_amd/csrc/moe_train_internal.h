@@ -37,6 +37,7 @@ struct GradWeightArgs {
     float *partial;                // workspace: [E, splits, n, k], then [E, splits, n]
     int32_t a_quant, dw_bf16, accumulate, splits;
     int32_t E, n, k, dense_rows;
+    int64_t max_rows;              // as above (chooses the tiles)
 };
 // Parts that an expert's rows are split into (1: no workspace).
 int32_t grad_weight_splits(int64_t max_rows, int32_t E, int32_t n, int32_t k);

@@ -28,9 +28,11 @@ using Weights256 = TileShape<256, 256, 2, 2, 32, 4>;
 // Four waves with 64 x 128, two blocks per compute unit; three stages.
 using Weights128 = TileShape<128, 256, 2, 2, 32, 3>;
 
-// Tiles along dy's channels that walk a's together.  32 experts x 1024 rows, 4096 x 7168,
-// 256 x 256: 4 / 6 / 8 of them 1823 / 1812 / 1862 us; 128 x 256: 4 / 8 / 16 / 32 of them 2032 /
-// 2007 / 1988 / 2052.
+// Tiles along dy's channels that walk a's together.  256 x 256, bf16 results, 4 / 5 / 6 / 8 of
+// them: 32 experts x 1024 rows, 4096 x 7168 1889 / 1884 / 1885 / 1917 us, 2048 x 7168 967 / 954 /
+// 963 / 982, 7168 x 2048 968 / 945 / 947 / 970; 8 experts x 4096 rows, 4096 x 4096 875 / 878 / 869 /
+// 862; 32,768 dense rows, 4096 x 7168 1459 / 1482 / 1466 / 1458; 8192^3, fp32 813 / 815 / 812 / 809.
+// 128 x 256, 32 experts, 4096 x 7168: 4 / 8 / 16 / 32 of them 2032 / 2007 / 1988 / 2052.
 template <typename S>
 constexpr int group_tiles() { return S::BM == 256 ? 5 : 16; }
 
@@ -473,10 +475,23 @@ int64_t weight_tiles(int32_t E, int32_t n, int32_t k, int32_t rows)
     return (int64_t)E * ((n + rows - 1) / rows) * ((k + 255) / 256);
 }
 
-// 256 x 256 from half the compute units on: two smaller blocks on each hide each other's
-// waits, but read a half more.  128 / 256: 8191 rows, 768 x 2048 (24 tiles of 256) 40 / 51
-// us; 32,768 rows, 4096 x 7168 (448) 1658 / 1391; 32 experts x 1024 rows 1975 / 1812.
-bool wide_weights(int32_t E, int32_t n, int32_t k) { return weight_tiles(E, n, k, 256) >= 128; }
+// 256 x 256 on one block per compute unit, or 128 x 256 on two, which hide each other's waits
+// and results but read a half more: whichever takes less, by rounds over the compute units.
+// In eighths of a step of a wide round a wide round takes 8 steps and 96, two narrow blocks
+// 9 and 76, one alone 5 and 64.  128 / 256 (bf16 rows, fp32 results, us): 8192 dense rows,
+// 64 wide tiles 82 / 157, 128 125 / 160, 144 182 / 154, 256 230 / 204, 272 304 / 349, 384 350 /
+// 378, 448 440 / 376; 2048 dense rows, 128 tiles 38 / 48, 448 128 / 120; 32 experts, 4096 x
+// 7168, 64 rows each 795 / 797 (bf16 results 444 / 580), 256 1231 / 1243 (831 / 937), 512 1696 /
+// 1544 (1210 / 1222), 1024 2487 / 2184 (2038 / 1900); 256 rows each, 768 x 768 (288 tiles) 27.5 /
+// 44.2; 8 experts x 512 rows, 2048 x 4096 104 / 110 (82 / 91).  Of 170 such pairs the rule takes the
+// slower side by more than 3% in four (at most 10%: 512 rows in many rounds).
+bool wide_weights(int64_t max_rows, int32_t E, int32_t n, int32_t k)
+{
+    const int64_t cus = device_cu_count(), steps = max_rows / E / Weights256::kStep;
+    const int64_t wide = weight_tiles(E, n, k, 256), narrow = weight_tiles(E, n, k, 128), left = narrow % (2 * cus);
+    const int64_t rounds = (wide + cus - 1) / cus, pairs = narrow / (2 * cus) + (left > cus), alone = left > 0 && left <= cus;
+    return rounds * (8 * steps + 96) <= pairs * (9 * steps + 76) + alone * (5 * steps + 64);
+}
 
 template <typename S>
 hipError_t launch_weights(const GradWeightArgs &p, hipStream_t stream)
@@ -506,19 +521,19 @@ hipError_t launch_weights(const GradWeightArgs &p, hipStream_t stream)
 
 int32_t grad_weight_splits(int64_t max_rows, int32_t E, int32_t n, int32_t k)
 {
-    if (wide_weights(E, n, k))
+    if (wide_weights(max_rows, E, n, k))  // never where narrow tiles alone leave compute units free
         return 1;
-    // 256 blocks, one per compute unit, of at least 512 rows: more of them write and read
-    // more parts (8191 rows, 768 x 2048, 48 tiles: 256 / 384 / 512 blocks 42 / 45 / 48 us;
-    // 2048 x 2048, 128 tiles: 81 / 93 / 88)
-    const int64_t most = max_rows / E / 512, splits = 256 / weight_tiles(E, n, k, 128);
+    // One block per compute unit, of at least 512 rows: more of them write and read more
+    // parts (8191 rows, 768 x 2048, 48 tiles: 256 / 384 / 512 blocks 42 / 45 / 48 us; 2048 x 2048,
+    // 128 tiles: 81 / 93 / 88)
+    const int64_t most = max_rows / E / 512, splits = device_cu_count() / weight_tiles(E, n, k, 128);
     return (int32_t)(splits < 1 || most < 1 ? 1 : splits < most ? splits : most);
 }
 
 hipError_t launch_grad_weight(const GradWeightArgs &p, hipStream_t stream)
 {
-    const hipError_t e = wide_weights(p.E, p.n, p.k) ? launch_weights<Weights256>(p, stream)
-                                                     : launch_weights<Weights128>(p, stream);
+    const hipError_t e = wide_weights(p.max_rows, p.E, p.n, p.k) ? launch_weights<Weights256>(p, stream)
+                                                                 : launch_weights<Weights128>(p, stream);
     if (e != hipSuccess || p.splits == 1)
         return e;
     const int64_t quads = (int64_t)p.E * p.n * p.k / 4, all = quads + (p.dbias != nullptr ? (int64_t)p.E * p.n / 4 : 0);

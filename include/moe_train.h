@@ -151,9 +151,9 @@ moe_status_t moe_expert_grad_weight(const moe_config_t *cfg, int32_t num_tokens,
                                     const moe_handle_t *handle, void *dw, int32_t dw_bf16, float *dbias,
                                     int32_t accumulate, void *workspace, size_t workspace_bytes, void *stream);
 
-/* Bytes of device workspace moe_expert_grad_weight needs for num_tokens tokens
- * (few weights share their rows' sums among more of the chip and join them
- * there; 0 for most sizes).  0 for arguments that it refuses. */
+/* Bytes of device workspace moe_expert_grad_weight needs for num_tokens tokens on
+ * the current device (few weights share their rows' sums among more of the chip
+ * and join them there; 0 for most sizes).  0 for arguments that it refuses. */
 size_t moe_grad_weight_workspace_bytes(const moe_config_t *cfg, int32_t num_tokens, int32_t n, int32_t k);
 
 /*
