@@ -20,7 +20,8 @@ __device__ __forceinline__ float gelu_z(float v) { return v * (kGeluLinear + kGe
 // 1 / (1 + exp(-z)) from the hardware's exp2 and reciprocal (1 step each): the
 // argument's rounding costs |z| 2^-24 of exp(-z), which s (1 - s) damps to less than
 // 2^-24 of 1 where s matters beside 1, and |z| 2^-24 < 2^-17 of s itself where it
-// does not: far below bf16's half step of 2^-9.  Where exp overflows s is 0.
+// does not: far below bf16's half step of 2^-8.  The reciprocal has no subnormal
+// results: s is 0 where it is below 2^-126, z < -87.3.
 __device__ __forceinline__ float sigmoid(float z)
 {
     return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(z * -1.4426950408889634f));

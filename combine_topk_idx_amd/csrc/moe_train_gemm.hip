@@ -710,12 +710,15 @@ hipError_t launch_product(const TrainGemmArgs &p, hipStream_t stream)
     const bool quantized = p.saved != nullptr && p.saved_quant != MOE_QUANT_NONE;
     if constexpr (P != kGradInput) {
         // Strips for up to 32 rows per expert, while three blocks per compute unit hold them
-        // all (in a graph, 64-row tiles / strips): one row, 7168 -> 4096 (256 strips) 38 / 13.6
-        // us, 2048 -> 7168 (448) 14.7 / 11.0; 16 rows, 512 -> 512 (32) 7.0 / 6.1; 32 rows, 7168 ->
-        // 4096 (512) 38 / 26, 2048 -> 2048 (256) 14.7 / 12.0; 64 rows, 2048 -> 2048 (512) 12.6 /
-        // 18.3; 8 experts, 2048 -> 1024, 2 rows each (576) 15.4 / 12.7, 16 rows (1024) 15.5 /
-        // 23.8.  8-bit saved rows need the 128 channels of a block together, which strips do not
-        // have.
+        // all (in a graph, the same weights again, 64-row tiles / strips): one row, 7168 -> 4096
+        // (256 strips) 38 / 13.6 us, 2048 -> 7168 (448) 14.7 / 11.0; 16 rows, 512 -> 512 (32) 7.0 /
+        // 6.1; 32 rows, 7168 -> 4096 (512) 38 / 26, 2048 -> 2048 (256) 14.7 / 12.0; 8 experts, 2048 ->
+        // 1024, 2 rows each (576) 15.4 / 12.7, 16 rows (1024) 15.5 / 23.8.  More rows take 64-row
+        // tiles whatever their number: strips of 32 rows lose as soon as there are more of them
+        // than compute units (64 rows, 2048 -> 4096 12.5 / 22.8, 7168 -> 4096 39 / 49; 96 rows, 2048 ->
+        // 2048 14.6 / 22.3), and gain below that only with many summed channels (64 rows, 512 -> 512
+        // 7.1 / 7.9, 2048 -> 2048 12.5 / 12.0, 7168 -> 2048 38 / 26).  8-bit saved rows need the 128
+        // channels of a block together, which strips do not have.
         const int32_t strips = P == kGated ? p.n / 16 : (p.n + 15) / 16;
         const int64_t rows = (p.max_rows + p.E - 1) / p.E;
         if (!quantized && rows <= 32 && max_tiles(p, 16) * strips <= 3 * cus)

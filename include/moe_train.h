@@ -63,6 +63,8 @@ extern "C" {
 #define MOE_ACT_SILU 1 /* v / (1 + exp(-v)) */
 #define MOE_ACT_GELU 2 /* v / 2 (1 + tanh(sqrt(2/pi) (v + 0.044715 v^3))) */
 #define MOE_ACT_RELU 3 /* v > 0 ? v : 0 (slope 0 at 0) */
+/* Where 1 / (1 + exp(-z)) is below 2^-126 (z = v for SiLU, sqrt(8/pi) (v + 0.044715 v^3)
+ * for GELU; v < -87.3 and v < -10) both and their slopes are 0. */
 
 /*
  * The gated block: for every row of expert e, with p = a . w13[e] and g, u its
