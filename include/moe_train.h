@@ -46,6 +46,8 @@
  * Saved rows.  The input of an activation can be kept for its gradient, in
  * saved_quant's format: MOE_QUANT_NONE, bf16 rows (saved_scale NULL), or E4M3
  * rows with scales as moe_dispatch writes them (channels then a multiple of 128).
+ * Scales follow the fp32 sums: a block whose largest value lies within their error of
+ * a format's border (448 times a power of two) may take the scale on either side.
  */
 #ifndef MOE_TRAIN_H
 #define MOE_TRAIN_H
