@@ -94,6 +94,26 @@ def test_grad_weight_accumulates(layout, n, k, quant):
         R.assert_near(db[e], bold + sv, sb + (bold.abs() + sv.abs()) * 2.0 ** -23, "dbias")
 
 
+@pytest.mark.parametrize("T,n,k,shared", [(1100, 64, 32768, True), (1100, 136, 16384, True), (1100, 64, 33024, False),
+                                          (500, 64, 32768, False)])
+def test_rows_are_shared_up_to_half_the_compute_units(T, n, k, shared):
+    """128 tiles of weights share their rows between two blocks each from 1024 rows on, 129 do not (256 compute units)."""
+    _say(f"grad weight shared rows T={T} n={n} k={k}")
+    rows = Rows(T)
+    size = M.moe_grad_weight_workspace_bytes(rows.cfg, T, n, k)
+    if torch.cuda.get_device_properties(0).multi_processor_count == 256:
+        assert size == (2 * (n * k + n) * 4 if shared else 0)
+    g = _gen(k)
+    dy, a = rows.input(g, n, 0.02), rows.input(g, k)
+    dw, db = _filled((2, n, k), torch.float32), _filled((2, n), torch.float32)
+    _grad_weight(rows, n, k, dy, a, None, BF16, dw, db)
+    for _, (v, b), (sv, sb) in _grad_weight_reference(rows, dy, a, None, BF16):
+        R.assert_near(dw[0], v, b, "dw")
+        R.assert_near(db[0], sv, sb, "dbias")
+    _untouched(dw[1], "dw behind the last expert")
+    _untouched(db[1], "dbias behind the last expert")
+
+
 @pytest.mark.parametrize("quant", [BF16, UE8M0])
 def test_tiles_agree_on_shared_channels(quant):
     """The first 256 x 512 weights of a large product and the same ones alone: other tiles, the same bits, for each sums
